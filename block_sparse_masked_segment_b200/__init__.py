@@ -24,6 +24,15 @@ from ._abi import (  # noqa: F401
     opr_kpass,
     opr_loss_rows,
     opr_cross_entropy,
+    opr_rotary_frequencies,
+    opr_rotary,
+    opr_qk_norm_rope,
+    opr_qk_norm_rope_bwd,
+    opr_qk_norm_rope_bwd_workspace_bytes,
+    opr_linear,
+    opr_linear_workspace_bytes,
+    opr_linear_bwd,
+    opr_linear_bwd_workspace_bytes,
     KPass,
     BWD_ROW_TERMS,
     BWD_DQ,
@@ -36,6 +45,6 @@ from ._abi import (  # noqa: F401
     layout_table_offsets,
     EXPORTED_SYMBOLS,
 )
-from .pipeline import OnePassAttention, one_pass_forward, one_pass_backward, useful_flops  # noqa: F401
+from .pipeline import OnePassAttention, OnePassAttentionLayer, one_pass_forward, one_pass_backward, useful_flops  # noqa: F401
 
 __version__ = "0.1.0"

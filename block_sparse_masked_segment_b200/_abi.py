@@ -49,6 +49,15 @@ EXPORTED_SYMBOLS = (
     "opr_loss_row_count",
     "opr_loss_rows",
     "opr_cross_entropy",
+    "opr_rotary_frequencies",
+    "opr_rotary",
+    "opr_qk_norm_rope",
+    "opr_qk_norm_rope_bwd_workspace_bytes",
+    "opr_qk_norm_rope_bwd",
+    "opr_linear_workspace_bytes",
+    "opr_linear",
+    "opr_linear_bwd_workspace_bytes",
+    "opr_linear_bwd",
     "opr_testing_set_wait_limit_ns",
     "opr_testing_layout_tables",
 )
@@ -131,6 +140,28 @@ def load_library() -> ctypes.CDLL:
     lib.opr_attn_bwd_noalloc.restype = I32
     lib.opr_attn_bwd_noalloc.argtypes = [P, P, P, I32, P, I32, P, P, P, P, P, I32, I32, I32, I64, I32, I32, I32, I32,
                                          F, P, P, P, P, D, P, P]
+    lib.opr_rotary_frequencies.restype = I32
+    lib.opr_rotary_frequencies.argtypes = [I32, D, I32, D, D, D, D, P, P]
+    lib.opr_rotary.restype = I32
+    lib.opr_rotary.argtypes = [P, I32, I64, P, I32, I64, P, P, I32, I32, F, I32, P, I64, I32, I32, P, P]
+    lib.opr_qk_norm_rope.restype = I32
+    lib.opr_qk_norm_rope.argtypes = [P, I64, P, I64, P, I64, I32, P, P, I32, F, P, P, I32, I32, F, P, I64, I32, I32,
+                                     I32, P, P, P, I32, P, P]
+    lib.opr_qk_norm_rope_bwd_workspace_bytes.restype = SZ
+    lib.opr_qk_norm_rope_bwd_workspace_bytes.argtypes = [I64, I32, I32, I32]
+    lib.opr_qk_norm_rope_bwd.restype = I32
+    lib.opr_qk_norm_rope_bwd.argtypes = [P, P, P, I32, P, I64, P, I64, I32, P, P, I32, F, P, P, I32, I32, F, P, I64,
+                                         I32, I32, I32, P, I64, P, I64, P, I64, I32, P, P, P, SZ, P, P]
+    lib.opr_linear_workspace_bytes.restype = SZ
+    lib.opr_linear_workspace_bytes.argtypes = [P, I64, P, I64, I64, I32, I32]
+    lib.opr_linear.restype = I32
+    lib.opr_linear.argtypes = [P, I64, P, I64, I32, P, I32, I32, P, I64, I32, P, I64, I32, P, I64, I64, I32, I32, P,
+                               SZ, P, P]
+    lib.opr_linear_bwd_workspace_bytes.restype = SZ
+    lib.opr_linear_bwd_workspace_bytes.argtypes = [P, I64, P, I64, P, I64, I64, I32, I32, I32]
+    lib.opr_linear_bwd.restype = I32
+    lib.opr_linear_bwd.argtypes = [P, I64, P, I64, P, I64, I32, P, I64, I32, P, I64, I32, P, I64, I32, P, I64, I32, P,
+                                   I64, I32, I32, P, SZ, P, P]
     _lib = lib
     return lib
 
@@ -582,3 +613,348 @@ def opr_cross_entropy(logits: torch.Tensor, target_ids: torch.Tensor, grad_scale
            "opr_cross_entropy")
     loss._status = status
     return loss, dl
+
+
+# ------------------------------------------------------------------ the layer around the attention
+ROTARY_RULES = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+def opr_rotary_frequencies(rot_dim: int, base: float, rule: str = "plain", factor: float = 1.0,
+                           original_length: float = 0.0, low_turns: float = 1.0, high_turns: float = 32.0,
+                           device="cuda") -> tuple[torch.Tensor, float]:
+    """(freq fp64 [rot_dim / 2] on ``device``, factor on the rotated values) of a scaling rule: "plain",
+    "linear", "ntk", "yarn" or "wavelength" (include/opr.h has the formulas).  The table is what opr_rotary
+    and opr_qk_norm_rope take; keep it for as long as the model uses the rule."""
+    if rule not in ROTARY_RULES:
+        raise OprError(f"rule must be one of {', '.join(ROTARY_RULES)}")
+    freq = np.empty(max(int(rot_dim) // 2, 1), dtype=np.float64)
+    scale = ctypes.c_double(0.0)
+    _check(load_library().opr_rotary_frequencies(int(rot_dim), float(base), ROTARY_RULES[rule], float(factor),
+                                                 float(original_length), float(low_turns), float(high_turns),
+                                                 freq.ctypes.data, ctypes.byref(scale)), "opr_rotary_frequencies")
+    return torch.from_numpy(freq).to(device), scale.value
+
+
+def _heads(name: str, t: torch.Tensor, total: int | None = None, d: int | None = None,
+           heads: int | None = None) -> int:
+    """Checks rows of heads [total, heads, head_dim] (the heads of a token contiguous); their stride."""
+    if t.dim() != 3 or t.dtype not in _DT:
+        raise OprError(f"{name} must be bf16, fp16 or fp32 [tokens, heads, head_dim]")
+    if not t.is_cuda:
+        raise OprError("tensors must live on a CUDA device")
+    for want, got in ((total, t.shape[0]), (heads, t.shape[1]), (d, t.shape[2])):
+        if want is not None and want != got:
+            raise OprError(f"{name} has shape {tuple(t.shape)}, which does not fit the other tensors")
+    width = t.shape[1] * t.shape[2]
+    if t.numel() == 0 or t.shape[0] == 1 and t[0].is_contiguous():
+        return width
+    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]) or t.stride(0) < width:
+        raise OprError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0)
+
+
+def _one_device(call: str, first: torch.Tensor, *ts: torch.Tensor | None) -> None:
+    if any(t is not None and t.device != first.device for t in ts):
+        raise OprError(f"{call}: every tensor must be on one device")
+
+
+def _rotation(call: str, x: torch.Tensor, pos_id, freq, row_map, dev_status) -> None:
+    total = x.shape[0]
+    _need_cuda(pos_id, freq, *(() if row_map is None else (row_map,)))
+    if pos_id.dtype != torch.int32 or pos_id.numel() != total:
+        raise OprError("pos_id must be int32 with one entry per token")
+    if row_map is not None and (row_map.dtype != torch.int32 or row_map.numel() != total):
+        raise OprError("row_map must be int32 with one entry per token")
+    if freq.dtype != torch.float64 or freq.dim() != 1:
+        raise OprError("freq must be fp64 [rot_dim / 2] (opr_rotary_frequencies)")
+    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.numel() < 1):
+        raise OprError("dev_status must be an int32 word")
+    _one_device(call, x, pos_id, freq, row_map, dev_status)
+
+
+def opr_rotary(x: torch.Tensor, pos_id: torch.Tensor, freq: torch.Tensor, interleaved: bool = False,
+               scale: float = 1.0, inverse: bool = False, out: torch.Tensor | None = None,
+               dev_status: torch.Tensor | None = None, row_map: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotate the first 2 * len(freq) entries of each head of x [tokens, heads, head_dim] by
+    ``pos_id * freq`` into ``out`` (default: in place) and pass the others through.
+
+    ``interleaved`` pairs entries (2j, 2j + 1) instead of (j, j + len(freq)); ``scale`` multiplies the rotated
+    entries; ``inverse`` is the transpose (the gradient).  x and out may be parts of wider rows (the heads of a
+    token contiguous) and differ in type.  ``row_map`` sends row t to row row_map[t] of out (out must not be x).
+    """
+    out = x if out is None else out
+    xs, ys = _heads("x", x), _heads("out", out)
+    if out.shape != x.shape:
+        raise OprError("opr_rotary: out must have the shape of x")
+    _rotation("opr_rotary", x, pos_id, freq, row_map, dev_status)
+    _one_device("opr_rotary", x, out)
+    total, heads, d = x.shape
+    with torch.cuda.device(x.device):
+        st = load_library().opr_rotary(_ptr(x), _DT[x.dtype], xs, _ptr(out), _DT[out.dtype], ys, _ptr(pos_id),
+                                       _ptr(freq), 2 * freq.numel(), int(bool(interleaved)), float(scale),
+                                       int(bool(inverse)), _ptr(row_map), total, heads, d, _ptr(dev_status),
+                                       _stream(x.device))
+    _check(st, "opr_rotary")
+    return out
+
+
+def _norm_weights(q, k, q_weight, k_weight):
+    d = q.shape[2]
+    _need_cuda(q_weight, k_weight)
+    if q_weight.dtype not in _DT or k_weight.dtype != q_weight.dtype:
+        raise OprError("q_weight and k_weight must be bf16, fp16 or fp32, of one type")
+    if q_weight.shape != (d,) or k_weight.shape != (d,):
+        raise OprError("q_weight and k_weight must have head_dim entries")
+    if k.dtype != q.dtype:
+        raise OprError("q and k must have one type")
+
+
+def opr_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                     pos_id: torch.Tensor, freq: torch.Tensor, eps: float = 1e-6, interleaved: bool = False,
+                     scale: float = 1.0, v: torch.Tensor | None = None, out=None, out_dtype=torch.float16,
+                     row_map: torch.Tensor | None = None, dev_status: torch.Tensor | None = None):
+    """The attention's operands from the projections, in one pass: each head h of q and k becomes
+    ``h / sqrt(mean(h^2) + eps) * weight``, rotated as by opr_rotary; v is converted.
+
+    q [tokens, hq, head_dim], k and v [tokens, hkv, head_dim], which may be parts of one projection's rows.
+    Returns (q_out, k_out), with v (q_out, k_out, v_out), contiguous, of ``out_dtype``; row t is row
+    row_map[t] of them (a layout's attn_pos).  ``out`` = the same tuple reuses buffers.
+    """
+    qs = _heads("q", q)
+    total, hq, d = q.shape
+    ks = _heads("k", k, total, d)
+    vs = 0 if v is None else _heads("v", v, total, d, k.shape[1])
+    _norm_weights(q, k, q_weight, k_weight)
+    if v is not None and v.dtype != q.dtype:
+        raise OprError("q, k and v must have one type")
+    _rotation("opr_qk_norm_rope", q, pos_id, freq, row_map, dev_status)
+    ins = (q, k) if v is None else (q, k, v)
+    if out is None:
+        if out_dtype not in _DT:
+            raise OprError("out_dtype must be bf16, fp16 or fp32")
+        out = tuple(torch.empty(t.shape, dtype=out_dtype, device=q.device) for t in ins)
+    if len(out) != len(ins):
+        raise OprError("out must be (q_out, k_out), with v (q_out, k_out, v_out)")
+    _need_cuda(*out)
+    if any(o.shape != t.shape or o.dtype not in _DT or o.dtype != out[0].dtype for o, t in zip(out, ins)):
+        raise OprError("out must have the shapes of q, k and v and one type of bf16, fp16 or fp32")
+    _one_device("opr_qk_norm_rope", q, k, v, q_weight, k_weight, *out)
+    with torch.cuda.device(q.device):
+        st = load_library().opr_qk_norm_rope(
+            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _DT[q.dtype], _ptr(q_weight), _ptr(k_weight), _DT[q_weight.dtype],
+            float(eps), _ptr(pos_id), _ptr(freq), 2 * freq.numel(), int(bool(interleaved)), float(scale),
+            _ptr(row_map), total, hq, k.shape[1], d, _ptr(out[0]), _ptr(out[1]), _ptr(out[2]) if v is not None else None,
+            _DT[out[0].dtype], _ptr(dev_status), _stream(q.device))
+    _check(st, "opr_qk_norm_rope")
+    return tuple(out)
+
+
+def opr_qk_norm_rope_bwd_workspace_bytes(total_tokens, hq, hkv, head_dim) -> int:
+    return int(load_library().opr_qk_norm_rope_bwd_workspace_bytes(total_tokens, hq, hkv, head_dim))
+
+
+def opr_qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                         q_weight: torch.Tensor, k_weight: torch.Tensor, pos_id: torch.Tensor, freq: torch.Tensor,
+                         eps: float = 1e-6, interleaved: bool = False, scale: float = 1.0,
+                         dv: torch.Tensor | None = None, out=None, out_dtype=None,
+                         row_map: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         dev_status: torch.Tensor | None = None):
+    """Gradient of opr_qk_norm_rope: (dq_in, dk_in, [dv_in,] dq_weight, dk_weight) from the gradients dq, dk
+    (and dv) of its outputs and its inputs q, k.  dq_in, dk_in and dv_in have ``out_dtype`` (default: q's type)
+    or are the tensors of ``out``, which may be parts of one projection's gradient rows; the weights' gradients
+    are fp32.  With ``row_map`` the gradients of token t are rows row_map[t] of dq, dk and dv."""
+    qs = _heads("q", q)
+    total, hq, d = q.shape
+    ks = _heads("k", k, total, d)
+    hkv = k.shape[1]
+    _norm_weights(q, k, q_weight, k_weight)
+    _rotation("opr_qk_norm_rope_bwd", q, pos_id, freq, row_map, dev_status)
+    grads = (dq, dk) if dv is None else (dq, dk, dv)
+    shapes = (q.shape, k.shape, k.shape)
+    _need_cuda(*grads)
+    if any(g.shape != sh or g.dtype not in _DT or g.dtype != dq.dtype for g, sh in zip(grads, shapes)):
+        raise OprError("dq, dk and dv must have the shapes of q, k and v and one type of bf16, fp16 or fp32")
+    if out is None:
+        out_dtype = q.dtype if out_dtype is None else out_dtype
+        if out_dtype not in _DT:
+            raise OprError("out_dtype must be bf16, fp16 or fp32")
+        out = tuple(torch.empty(g.shape, dtype=out_dtype, device=q.device) for g in grads)
+    if len(out) != len(grads):
+        raise OprError("out must be (dq_in, dk_in), with dv (dq_in, dk_in, dv_in)")
+    strides = [_heads("out", o, total, d, g.shape[1]) for o, g in zip(out, grads)]
+    if any(o.dtype != out[0].dtype for o in out):
+        raise OprError("the tensors of out must have one type")
+    _one_device("opr_qk_norm_rope_bwd", q, k, q_weight, k_weight, *grads, *out)
+    wb = max(opr_qk_norm_rope_bwd_workspace_bytes(total, hq, hkv, d), 256)
+    if workspace is None:
+        workspace = torch.empty(wb, dtype=torch.uint8, device=q.device)
+    _need_cuda(workspace)
+    _one_device("opr_qk_norm_rope_bwd", q, workspace)
+    dqw, dkw = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in range(2))
+    with torch.cuda.device(q.device):
+        st = load_library().opr_qk_norm_rope_bwd(
+            _ptr(dq), _ptr(dk), _ptr(dv), _DT[dq.dtype], _ptr(q), qs, _ptr(k), ks, _DT[q.dtype], _ptr(q_weight),
+            _ptr(k_weight), _DT[q_weight.dtype], float(eps), _ptr(pos_id), _ptr(freq), 2 * freq.numel(),
+            int(bool(interleaved)), float(scale), _ptr(row_map), total, hq, hkv, d, _ptr(out[0]), strides[0],
+            _ptr(out[1]), strides[1], _ptr(out[2]) if dv is not None else None, strides[2] if dv is not None else 0,
+            _DT[out[0].dtype], _ptr(dqw), _ptr(dkw), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _ptr(dev_status), _stream(q.device))
+    _check(st, "opr_qk_norm_rope_bwd")
+    return (*out, dqw, dkw)
+
+
+def _matrix(name: str, t: torch.Tensor, dtypes=None, shape=None) -> int:
+    """Checks a matrix of contiguous rows; elements from row to row."""
+    if t.dim() != 2 or t.dtype not in (_DT if dtypes is None else dtypes):
+        raise OprError(f"{name} must be a matrix of " + " or ".join(
+            str(x).replace("torch.", "") for x in (_DT if dtypes is None else dtypes)))
+    if not t.is_cuda:
+        raise OprError("tensors must live on a CUDA device")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise OprError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.numel() == 0 or (t.shape[0] == 1 and t[0].is_contiguous()):
+        return max(t.shape[1], 1)
+    if (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < t.shape[1]:
+        raise OprError(f"{name}: rows must be contiguous")
+    return t.stride(0)
+
+
+def _status_word(dev_status, device) -> torch.Tensor:
+    if dev_status is None:
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    if dev_status.dtype != torch.int32 or dev_status.numel() < 1 or dev_status.device != device:
+        raise OprError(f"dev_status must be an int32 word on {device}")
+    return dev_status
+
+
+def _scratch(workspace, need: int, device):
+    """The caller's workspace, or one of `need` bytes (None for 0): (tensor, bytes)."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise OprError(f"workspace must be contiguous on {device}")
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+_MMA_TYPES = (torch.bfloat16, torch.float16)
+
+
+def opr_linear_workspace_bytes(x: torch.Tensor, w: torch.Tensor) -> int:
+    """Bytes of workspace opr_linear(x, w) needs: 0 where the rows of both start on 16-byte boundaries."""
+    ldx, ldw = _matrix("x", x, _MMA_TYPES), _matrix("w", w, _MMA_TYPES)
+    return int(load_library().opr_linear_workspace_bytes(_ptr(x), ldx, _ptr(w), ldw, x.shape[0], w.shape[0],
+                                                         x.shape[1]))
+
+
+def opr_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, activation: str | None = None,
+               residual: torch.Tensor | None = None, out: torch.Tensor | None = None, out_dtype=None,
+               save_z: bool = False, workspace: torch.Tensor | None = None,
+               dev_status: torch.Tensor | None = None):
+    """act(x w^T + bias) + residual for x [m, k] and w [n, k] of bf16 or fp16 (one type).
+
+    ``activation`` None, "silu", "gelu" or "gelu_tanh"; bias [n] and residual [m, n] of bf16, fp16 or fp32.  The
+    result has ``out_dtype`` (default: x's type) or is ``out``, which may be the residual.  With ``save_z``
+    returns (y, z), z = x w^T + bias in x's type, for opr_linear_bwd.  x, w, residual and out may be parts of
+    wider rows.  ``dev_status`` reports a pipeline timeout or an fp16 overflow (read_status).
+    """
+    ldx, ldw = _matrix("x", x, _MMA_TYPES), _matrix("w", w, (x.dtype,))
+    m, k = x.shape
+    n = w.shape[0]
+    if w.shape[1] != k:
+        raise OprError("x and w must have rows of one length")
+    if activation not in ACTIVATIONS:
+        raise OprError("activation must be one of None, " + ", ".join(a for a in ACTIVATIONS if a))
+    if bias is not None:
+        _need_cuda(bias)
+        if bias.shape != (n,) or bias.dtype not in _DT:
+            raise OprError("bias must be bf16, fp16 or fp32 with one entry per row of w")
+    ldr = 0 if residual is None else _matrix("residual", residual, shape=(m, n))
+    if out is None:
+        out_dtype = x.dtype if out_dtype is None else out_dtype
+        if out_dtype not in _DT:
+            raise OprError("out_dtype must be bf16, fp16 or fp32")
+        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
+    ldy = _matrix("out", out, shape=(m, n))
+    z = torch.empty((m, n), dtype=x.dtype, device=x.device) if save_z else None
+    _one_device("opr_linear", x, w, bias, residual, out)
+    status = _status_word(dev_status, x.device)
+    lib = load_library()
+    need = int(lib.opr_linear_workspace_bytes(_ptr(x), ldx, _ptr(w), ldw, m, n, k))
+    workspace, ws_bytes = _scratch(workspace, need, x.device)
+    with torch.cuda.device(x.device):
+        st = lib.opr_linear(_ptr(x), ldx, _ptr(w), ldw, _DT[x.dtype], _ptr(bias), 0 if bias is None else _DT[bias.dtype],
+                            ACTIVATIONS[activation], _ptr(residual), ldr,
+                            0 if residual is None else _DT[residual.dtype], _ptr(out), ldy, _DT[out.dtype], _ptr(z), n,
+                            m, n, k, _ptr(workspace), ws_bytes, _ptr(status), _stream(x.device))
+    _check(st, "opr_linear")
+    return (out, z) if save_z else out
+
+
+def opr_linear_bwd_workspace_bytes(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                                   activation: str | None = None) -> int:
+    """Bytes of workspace opr_linear_bwd(dy, x, w, activation=activation) needs."""
+    if activation not in ACTIVATIONS:
+        raise OprError("activation must be one of None, " + ", ".join(a for a in ACTIVATIONS if a))
+    lds = [_matrix(name, t, _MMA_TYPES) for name, t in (("dy", dy), ("x", x), ("w", w))]
+    return int(load_library().opr_linear_bwd_workspace_bytes(_ptr(dy), lds[0], _ptr(x), lds[1], _ptr(w), lds[2],
+                                                             x.shape[0], w.shape[0], x.shape[1],
+                                                             ACTIVATIONS[activation]))
+
+
+def opr_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.Tensor | None = None,
+                   activation: str | None = None, dx_residual: torch.Tensor | None = None, bias: bool = False,
+                   need_dx: bool = True, need_dw: bool = True, out=(None, None), dx_dtype=None, dw_dtype=None,
+                   workspace: torch.Tensor | None = None, dev_status: torch.Tensor | None = None):
+    """(dx, dw, db) of opr_linear: dz = dy act'(z), dx = dz w + dx_residual, dw = dz^T x, db = sum of dz over
+    the rows (fp32, with ``bias``); None for what is not asked for.
+
+    dy, x and w have one type of bf16 or fp16; z is opr_linear's (needed with an activation).  dx and dw have
+    ``dx_dtype`` and ``dw_dtype`` (default: x's and w's type) or are the tensors of ``out`` = (dx, dw), parts of
+    wider rows allowed; dx may be dx_residual.  The gradient with respect to opr_linear's residual is dy itself.
+    """
+    ldx, ldw = _matrix("x", x, _MMA_TYPES), _matrix("w", w, (x.dtype,))
+    m, k = x.shape
+    n = w.shape[0]
+    if w.shape[1] != k:
+        raise OprError("x and w must have rows of one length")
+    ldy = _matrix("dy", dy, (x.dtype,), (m, n))
+    if activation not in ACTIVATIONS:
+        raise OprError("activation must be one of None, " + ", ".join(a for a in ACTIVATIONS if a))
+    if activation is not None and z is None:
+        raise OprError("z (opr_linear's, with save_z) is needed for the gradient of an activation")
+    z = z if activation is not None else None
+    ldz = 0 if z is None else _matrix("z", z, (x.dtype,), (m, n))
+    if dx_residual is not None and not need_dx:
+        raise OprError("dx_residual is added to dx, which is not asked for")
+    ldr = 0 if dx_residual is None else _matrix("dx_residual", dx_residual, shape=(m, k))
+
+    def result(given, wanted, dtype, shape):
+        if not wanted:
+            return None
+        if given is not None:
+            return given
+        if dtype not in _DT:
+            raise OprError("gradients are bf16, fp16 or fp32")
+        return torch.empty(shape, dtype=dtype, device=x.device)
+
+    dx = result(out[0], need_dx, x.dtype if dx_dtype is None else dx_dtype, (m, k))
+    dw = result(out[1], need_dw, w.dtype if dw_dtype is None else dw_dtype, (n, k))
+    db = torch.empty(n, dtype=torch.float32, device=x.device) if bias else None
+    ldx_out = 0 if dx is None else _matrix("dx", dx, shape=(m, k))
+    ldw_out = 0 if dw is None else _matrix("dw", dw, shape=(n, k))
+    _one_device("opr_linear_bwd", x, w, dy, z, dx_residual, dx, dw)
+    status = _status_word(dev_status, x.device)
+    lib = load_library()
+    need = int(lib.opr_linear_bwd_workspace_bytes(_ptr(dy), ldy, _ptr(x), ldx, _ptr(w), ldw, m, n, k,
+                                                  ACTIVATIONS[activation]))
+    workspace, ws_bytes = _scratch(workspace, need, x.device)
+    with torch.cuda.device(x.device):
+        st = lib.opr_linear_bwd(_ptr(dy), ldy, _ptr(x), ldx, _ptr(w), ldw, _DT[x.dtype], _ptr(z), ldz,
+                                ACTIVATIONS[activation], _ptr(dx_residual), ldr,
+                                0 if dx_residual is None else _DT[dx_residual.dtype], _ptr(dx), ldx_out,
+                                0 if dx is None else _DT[dx.dtype], _ptr(dw), ldw_out,
+                                0 if dw is None else _DT[dw.dtype], _ptr(db), m, n, k, _ptr(workspace), ws_bytes,
+                                _ptr(status), _stream(x.device))
+    _check(st, "opr_linear_bwd")
+    return dx, dw, db

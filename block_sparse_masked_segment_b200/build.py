@@ -25,7 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libopr.so")
 LIB_DEBUG = os.path.join(LIB_DIR, "libopr_debug.so")
-SOURCES = ["api.cu", "layout.cu", "rope.cu", "attn_fwd.cu", "attn_bwd.cu", "noalloc.cu", "duplicate.cu", "loss.cu"]
+SOURCES = ["api.cu", "layout.cu", "rope.cu", "attn_fwd.cu", "attn_bwd.cu", "noalloc.cu", "duplicate.cu", "loss.cu",
+           "layer_api.cu", "rotary.cu", "linear.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 

@@ -3,8 +3,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -67,6 +65,14 @@ opr_status record_cuda_error(cudaError_t e) {
   return OPR_CUDA_ERROR;
 }
 
+opr_status device_check() {
+  int dev = 0, major = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  return major == 10 ? OPR_OK : OPR_UNSUPPORTED;
+}
+
 namespace {
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -84,20 +90,6 @@ EncodeTiledFn encode_fn() {
   }
   return fn;
 }
-
-// One NVTX range per entry-point call (named after the call), so that a
-// profiler timeline shows where each library call's launches begin and end.
-// Without an attached tool the push and pop cost a branch each.
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-  CallRange(const CallRange&) = delete;
-  CallRange& operator=(const CallRange&) = delete;
-};
-
-opr_status cuda_fail(cudaError_t e) { return record_cuda_error(e); }
-
-opr_status status_of(cudaError_t e) { return e == cudaSuccess ? OPR_OK : cuda_fail(e); }
 
 opr_status map_fail() {
   g_cuda_error_text = "TMA tensor map encoding failed (cuTensorMapEncodeTiled)";
@@ -122,14 +114,6 @@ bool make_map(CUtensorMap* map, const void* ptr, int64_t total, int32_t heads, i
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-opr_status device_check() {
-  int dev = 0, major = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  if (e != cudaSuccess) return cuda_fail(e);
-  return major == 10 ? OPR_OK : OPR_UNSUPPORTED;
-}
 
 AttnParams base_params(const int32_t* cu_seqlens, const int32_t* conv_idx, const void* ws, int32_t n_seqs,
                        int32_t n_convs, int32_t n_turns, int64_t total, int32_t max_seqlen, int32_t hq, int32_t hkv,

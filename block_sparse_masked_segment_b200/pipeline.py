@@ -4,6 +4,10 @@ forward:  opr_rope(q), opr_rope(k) by the layout's position ids (bf16 in,
           fp16 out) -> opr_attn_fwd
 backward: opr_attn_bwd with the position ids, which rotates dq and dk back
           (the gradients w.r.t. the unrotated q and k)
+OnePassAttentionLayer puts the layer's projections, the norm of each head of q
+and k and any rotary variant around it:
+forward:  opr_linear (q, k and v) -> opr_qk_norm_rope -> opr_attn_fwd -> opr_linear
+backward: the same calls' gradients in reverse
 (One-Pass to Reason: positions from "位置 ID 策略", mask from "分块稀疏注意力掩码").
 Every numerical step runs in libopr's CUDA kernels; this module only orders the
 calls and keeps buffers.
@@ -14,7 +18,8 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from ._abi import Layout, opr_attn_bwd, opr_attn_fwd, opr_build_layout, opr_rope
+from ._abi import (Layout, OprError, opr_attn_bwd, opr_attn_fwd, opr_build_layout, opr_linear, opr_linear_bwd,
+                   opr_qk_norm_rope, opr_qk_norm_rope_bwd, opr_rope)
 
 
 def visible_pairs_closed_form(turn_lens, conv_turn_ptr) -> int:
@@ -84,3 +89,61 @@ class OnePassAttention:
 
     def backward(self, q_rot, k_rot, v, o, do, lse, scale=None):
         return one_pass_backward(q_rot, k_rot, v, o, do, lse, self.layout, self.base, scale)
+
+
+class OnePassAttentionLayer:
+    """The attention layer from hidden states to hidden states, bf16.
+
+    x [tokens, width] -> q, k, v = x w_qkv^T + b_qkv -> each head of q and k normed, weighted and rotated ->
+    masked attention -> o w_o^T + b_o + residual.  w_qkv [(hq + 2 hkv) head_dim, width] holds the rows of q, k
+    and v in that order, w_o [width, hq head_dim]; ``freq`` and ``rotary_scale`` come from
+    opr_rotary_frequencies.
+
+    >>> freq, s = opr.opr_rotary_frequencies(128, 1e6)
+    >>> layer = OnePassAttentionLayer(turn_lens, conv_turn_ptr, seq_conv_ptr, 32, 8, 128, freq, s)
+    >>> y, saved = layer.forward(x, w_qkv, w_o, q_weight, k_weight, residual=x_stream)
+    >>> grads = layer.backward(dy, saved)            # the residual's gradient is dy
+    """
+
+    def __init__(self, turn_lens, conv_turn_ptr, seq_conv_ptr, hq: int, hkv: int, head_dim: int, freq: torch.Tensor,
+                 rotary_scale: float = 1.0, interleaved: bool = False, eps: float = 1e-6, device="cuda"):
+        self.layout = opr_build_layout(turn_lens, conv_turn_ptr, seq_conv_ptr, device=device)
+        self.hq, self.hkv, self.head_dim = hq, hkv, head_dim
+        self.rotation = dict(pos_id=self.layout.pos_id, freq=freq, eps=eps, interleaved=interleaved,
+                             scale=rotary_scale)
+
+    def forward(self, x, w_qkv, w_o, q_weight, k_weight, b_qkv=None, b_o=None, residual=None, scale=None):
+        """(y, saved): saved is what backward takes (it refers to x and the weights, without copies)."""
+        lay, hq, hkv, d = self.layout, self.hq, self.hkv, self.head_dim
+        if x.dtype != torch.bfloat16:
+            raise OprError("OnePassAttentionLayer: x must be bf16")
+        if x.dim() != 2 or x.shape[0] != lay.total or w_qkv.shape[0] != (hq + 2 * hkv) * d:
+            raise OprError("OnePassAttentionLayer: x must have the layout's tokens and w_qkv the rows of q, k and v")
+        st, cut = lay.dev_status, (hq + hkv) * d
+        bias = (None, None) if b_qkv is None else (b_qkv[:cut], b_qkv[cut:])
+        # v apart from q and k: opr_attn_bwd takes it contiguous
+        qk = opr_linear(x, w_qkv[:cut], bias[0], dev_status=st).view(-1, hq + hkv, d)
+        v = opr_linear(x, w_qkv[cut:], bias[1], dev_status=st).view(-1, hkv, d)
+        q_rot, k_rot, v16 = opr_qk_norm_rope(qk[:, :hq], qk[:, hq:], q_weight, k_weight, **self.rotation, v=v,
+                                             row_map=lay.attn_pos, dev_status=st)
+        o, lse = opr_attn_fwd(q_rot, k_rot, v16, lay, scale, torch.bfloat16)
+        y = opr_linear(o.view(-1, hq * d), w_o, b_o, residual=residual, dev_status=st)
+        saved = dict(x=x, w_qkv=w_qkv, w_o=w_o, q_weight=q_weight, k_weight=k_weight, qk=qk, v=v, q_rot=q_rot,
+                     k_rot=k_rot, o=o, lse=lse, scale=scale, has_b_qkv=b_qkv is not None, has_b_o=b_o is not None)
+        return y, saved
+
+    def backward(self, dy, saved) -> dict:
+        """Gradients of x, w_qkv, w_o, q_weight, k_weight and of the biases that forward was given."""
+        lay, hq, hkv, d, s = self.layout, self.hq, self.hkv, self.head_dim, saved
+        st, qk = lay.dev_status, s["qk"]
+        do, dw_o, db_o = opr_linear_bwd(dy, s["o"].view(-1, hq * d), s["w_o"], bias=s["has_b_o"], dev_status=st)
+        # no rope_base: the gradients w.r.t. the rotated q and k, rotated back below with the norm's gradient
+        dq, dk, dv = opr_attn_bwd(s["q_rot"], s["k_rot"], s["v"], s["o"], do.view(-1, hq, d), s["lse"], lay,
+                                  s["scale"])
+        dqkv = torch.empty((lay.total, hq + 2 * hkv, d), dtype=torch.bfloat16, device=dy.device)
+        *_, dq_weight, dk_weight = opr_qk_norm_rope_bwd(
+            dq, dk, qk[:, :hq], qk[:, hq:], s["q_weight"], s["k_weight"], **self.rotation, dv=dv,
+            out=(dqkv[:, :hq], dqkv[:, hq:hq + hkv], dqkv[:, hq + hkv:]), dev_status=st)
+        dx, dw_qkv, db_qkv = opr_linear_bwd(dqkv.view(-1, (hq + 2 * hkv) * d), s["x"], s["w_qkv"],
+                                            bias=s["has_b_qkv"], dev_status=st)
+        return dict(x=dx, w_qkv=dw_qkv, w_o=dw_o, q_weight=dq_weight, k_weight=dk_weight, b_qkv=db_qkv, b_o=db_o)

@@ -511,6 +511,159 @@ OPR_API opr_status opr_cross_entropy(const void* logits, int32_t dtype, int64_t 
                                      const int32_t* target_ids, float* loss, void* dlogits,
                                      float grad_scale, int32_t* dev_status, void* stream);
 
+/*
+ * The operators around the attention in a layer: rotary positions in their general form, the
+ * norm of each head of q and k with the rotation in the same pass, and the matrix product of the
+ * projections.  They follow the formulas below, not a passage of the pages, which leave the
+ * layer's other parts to the model.
+ *
+ * Rows of heads: x [total_tokens, n_heads, head_dim] with x_stride elements from token to token
+ * (the heads of a token are contiguous), so that q, k and v may be parts of one projection's rows.
+ *
+ * opr_rotary_frequencies - host call: the frequency of each rotated pair, freq[rot_dim / 2] in
+ * radians per position (HOST memory), and the factor on the rotated values, for one of
+ *   OPR_ROTARY_PLAIN       f_j = base^(-2j / rot_dim)
+ *   OPR_ROTARY_LINEAR      f_j / factor
+ *   OPR_ROTARY_NTK         base replaced by base * factor^(rot_dim / (rot_dim - 2)); rot_dim > 2
+ *   OPR_ROTARY_YARN        f_j below pair index lo, f_j / factor above hi, linear in j between;
+ *                          lo, hi: the pairs that make high_turns and low_turns turns over
+ *                          original_length (lo rounded down, hi up, within [0, rot_dim - 1]).
+ *                          scale = 0.1 ln(factor) + 1 (1 for the other rules)
+ *   OPR_ROTARY_WAVELENGTH  f_j for pairs of at least high_turns turns over original_length,
+ *                          f_j / factor for at most low_turns, linear in the turns between
+ * rot_dim even, 2 .. 256; base > 1; factor >= 1; 0 < low_turns < high_turns.  Arguments that a
+ * rule does not use are ignored.  OPR_UNSUPPORTED for another rule.
+ */
+#define OPR_ROTARY_PLAIN 0
+#define OPR_ROTARY_LINEAR 1
+#define OPR_ROTARY_NTK 2
+#define OPR_ROTARY_YARN 3
+#define OPR_ROTARY_WAVELENGTH 4
+OPR_API opr_status opr_rotary_frequencies(int32_t rot_dim, double base, int32_t rule, double factor,
+                                          double original_length, double low_turns, double high_turns,
+                                          double* freq, double* scale);
+
+/*
+ * opr_rotary - rotary positions: either pair layout, all or the first rot_dim entries of a head,
+ * any table of frequencies.  Pair j is (x[j], x[j + rot_dim/2]), or (x[2j], x[2j+1]) when
+ * `interleaved` != 0; with angle t = pos_id * freq[j] (fp64)
+ *   y_a = scale (x_a cos t - x_b sin t),  y_b = scale (x_b cos t + x_a sin t)
+ * and entries from rot_dim on are passed through.  `inverse` != 0 applies the transpose (angle
+ * -t, the same scale): the gradient with respect to x from that with respect to y.
+ *   x, y      rows of heads of type x_dtype / y_dtype (bf16, fp16 or fp32); x_stride, y_stride
+ *             >= n_heads * head_dim
+ *   pos_id    int32 [total_tokens], of either sign
+ *   freq      fp64 [rot_dim / 2], device
+ *   row_map   NULL, or int32 [total_tokens], distinct entries: row t goes to row row_map[t] of y
+ *             (an entry named twice leaves either row, or parts of both, there).  An entry out of
+ *             range sets OPR_DEV_BAD_INPUT and its row is not written.
+ *   dev_status  may be NULL; otherwise also OPR_DEV_FP16_RANGE when an fp16 output overflows
+ * y may be x (same type and stride, no row_map); any other overlap is refused.  head_dim 2 .. 256,
+ * rot_dim even, 2 .. head_dim.  opr_rope is the case of the whole head, the half layout and
+ * OPR_ROTARY_PLAIN.
+ */
+OPR_API opr_status opr_rotary(const void* x, int32_t x_dtype, int64_t x_stride, void* y, int32_t y_dtype,
+                              int64_t y_stride, const int32_t* pos_id, const double* freq, int32_t rot_dim,
+                              int32_t interleaved, float scale, int32_t inverse, const int32_t* row_map,
+                              int64_t total_tokens, int32_t n_heads, int32_t head_dim, int32_t* dev_status,
+                              void* stream);
+
+/*
+ * opr_qk_norm_rope - the operands of opr_attn_fwd from the projections, in one pass: each head h
+ * of q and k becomes rotate(h / sqrt(mean(h^2) + eps) * weight) with the rotation of opr_rotary,
+ * v (may be NULL, then v_out too) is converted, and row t of all goes to row row_map[t]
+ * (opr_build_layout's attn_pos; NULL: row t).  fp32 arithmetic, one rounding.
+ *   q [total, hq, head_dim], k, v [total, hkv, head_dim]  rows of heads, x_dtype, strides >= heads
+ *                         * head_dim
+ *   q_weight, k_weight    [head_dim], w_dtype;  eps > 0
+ *   q_out, k_out, v_out   contiguous, y_dtype (fp16 for the attention calls)
+ * dev_status as in opr_rotary.  An output may replace its own input (same type and stride, no
+ * row_map); any other overlap is refused.
+ */
+OPR_API opr_status opr_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                    const void* v, int64_t v_stride, int32_t x_dtype, const void* q_weight,
+                                    const void* k_weight, int32_t w_dtype, float eps, const int32_t* pos_id,
+                                    const double* freq, int32_t rot_dim, int32_t interleaved, float scale,
+                                    const int32_t* row_map, int64_t total_tokens, int32_t hq, int32_t hkv,
+                                    int32_t head_dim, void* q_out, void* k_out, void* v_out, int32_t y_dtype,
+                                    int32_t* dev_status, void* stream);
+
+/*
+ * opr_qk_norm_rope_bwd - its gradient.  dq, dk, dv: the gradients of q_out, k_out, v_out,
+ * contiguous, dy_dtype (opr_attn_bwd without rope_pos_id leaves them in the stream order: pass
+ * row_map NULL; with a row_map, row row_map[t] is read for token t).  q, k, weights, eps, pos_id,
+ * freq: the forward call's.  Writes dq_out, dk_out, dv_out (rows of heads, dx_dtype, each with its
+ * own stride) and dq_weight, dk_weight fp32 [head_dim], summed over tokens and heads in a fixed
+ * order.  dv and dv_out may be NULL.  total_tokens = 0 sets the weight gradients to zero.
+ *   workspace  opr_qk_norm_rope_bwd_workspace_bytes(...), 16-byte aligned; calls that may run at
+ *              the same time need workspaces of their own
+ * dq_out may replace dq (contiguous, no row_map) or q, dk_out dk or k, dv_out dv, each with the same type
+ * and stride; any other overlap is refused.  A row_map entry out of range sets OPR_DEV_BAD_INPUT and
+ * its token is left out.
+ */
+OPR_API size_t opr_qk_norm_rope_bwd_workspace_bytes(int64_t total_tokens, int32_t hq, int32_t hkv,
+                                                    int32_t head_dim);
+OPR_API opr_status opr_qk_norm_rope_bwd(const void* dq, const void* dk, const void* dv, int32_t dy_dtype,
+                                        const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                        int32_t x_dtype, const void* q_weight, const void* k_weight,
+                                        int32_t w_dtype, float eps, const int32_t* pos_id,
+                                        const double* freq, int32_t rot_dim, int32_t interleaved, float scale,
+                                        const int32_t* row_map, int64_t total_tokens, int32_t hq, int32_t hkv,
+                                        int32_t head_dim, void* dq_out, int64_t dq_stride, void* dk_out,
+                                        int64_t dk_stride, void* dv_out, int64_t dv_stride, int32_t dx_dtype,
+                                        float* dq_weight, float* dk_weight, void* workspace,
+                                        size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * opr_linear - y = act(x w^T + bias) + residual, the projections of a layer (tcgen05).
+ *   x [m, k], w [n, k]   dtype OPR_DTYPE_BF16 or OPR_DTYPE_FP16; ldx, ldw elements from row to row
+ *   bias      [n], bias_dtype, or NULL
+ *   activation OPR_ACT_NONE, OPR_ACT_SILU z / (1 + e^-z), OPR_ACT_GELU z Phi(z),
+ *             OPR_ACT_GELU_TANH z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
+ *   residual  [m, n], residual_dtype, ld_residual, or NULL; may be y (same type and row length)
+ *   y         [m, n], y_dtype (bf16, fp16 or fp32), ldy
+ *   z         NULL, or [m, n] of type dtype: x w^T + bias, rounded, for opr_linear_bwd
+ * fp32 sums, act and residual on the unrounded sum, one rounding.  The tensor cores drop the bits
+ * below the running sum: over k = 4096 products of random signs the sum is off by 4e-6 of its size,
+ * over 16384 by 2e-5, which an fp32 y shows and a 16-bit one does not.
+ * Rows that start on 16-byte boundaries are read in place; an x or w with others is copied to the
+ * workspace first (opr_linear_workspace_bytes looks at the addresses, not at the data).
+ *   workspace 16-byte aligned, may be NULL when 0 bytes are needed; calls that may run at the same
+ *             time need workspaces of their own
+ *   dev_status required: OPR_DEV_WAIT_TIMEOUT, OPR_DEV_FP16_RANGE (an fp16 y or z overflows)
+ * m = 0 does nothing; n, k > 0; m < 2^31.  Outputs that overlap inputs or one another are refused.
+ */
+#define OPR_ACT_NONE 0
+#define OPR_ACT_SILU 1
+#define OPR_ACT_GELU 2
+#define OPR_ACT_GELU_TANH 3
+OPR_API size_t opr_linear_workspace_bytes(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t m,
+                                          int32_t n, int32_t k);
+OPR_API opr_status opr_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t dtype,
+                              const void* bias, int32_t bias_dtype, int32_t activation, const void* residual,
+                              int64_t ld_residual, int32_t residual_dtype, void* y, int64_t ldy,
+                              int32_t y_dtype, void* z, int64_t ldz, int64_t m, int32_t n, int32_t k,
+                              void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * opr_linear_bwd - its gradients: dz = dy act'(z), db = sum of dz over the rows (fp32, fixed order,
+ * before dz is rounded), dx = dz w + dx_residual, dw = dz^T x.
+ *   dy [m, n]  dtype;  z as kept by opr_linear (unused and may be NULL without an activation)
+ *   dx [m, k], dw [n, k], db [n]  each may be NULL: not computed.  dx_residual [m, k] or NULL;
+ *              may be dx (same type and row length).  m = 0 sets dw and db to zero.
+ * With an activation dz is rounded to dtype for the two products (the type of their operands).
+ * Workspace, dev_status, alignment and overlap as in opr_linear.
+ */
+OPR_API size_t opr_linear_bwd_workspace_bytes(const void* dy, int64_t ld_dy, const void* x, int64_t ldx,
+                                              const void* w, int64_t ldw, int64_t m, int32_t n, int32_t k,
+                                              int32_t activation);
+OPR_API opr_status opr_linear_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const void* w,
+                                  int64_t ldw, int32_t dtype, const void* z, int64_t ldz, int32_t activation,
+                                  const void* dx_residual, int64_t ld_residual, int32_t residual_dtype,
+                                  void* dx, int64_t ld_dx, int32_t dx_dtype, void* dw, int64_t ld_dw,
+                                  int32_t dw_dtype, float* db, int64_t m, int32_t n, int32_t k,
+                                  void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
 OPR_API const char* opr_version(void);
 
 /*

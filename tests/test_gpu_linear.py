@@ -1,0 +1,237 @@
+"""opr_linear and opr_linear_bwd on the GPU against the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_masked_segment_b200 as opr
+from block_sparse_masked_segment_b200 import _abi
+from layer_helpers import TYPES, half_step, matrix, to64, within
+from oracle import layer_oracle as lo
+
+pytestmark = pytest.mark.gpu
+
+
+def status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def sum_bound(a, b, k):
+    """Of a sum of k exact products: the tensor cores add sixteen at a time and may drop up to two of the
+    running sum's last bits (2^-22) each time; the running sum is at most the sum of the sizes."""
+    return (np.abs(a) @ np.abs(b).T) * (k / 16 + 8) * 2.0 ** -22
+
+
+# |act'| <= 1.13 for all three; the functions themselves within 2^-20 of |z| + 1
+def act_bound(z, bz, activation):
+    return bz if activation is None else 1.13 * bz + (np.abs(z) + 1) * 2.0 ** -20
+
+
+SHAPES = [(1, 8, 8), (1, 1, 1), (2, 130, 64), (1, 256, 1000), (7, 3, 5), (16, 512, 513), (33, 64, 96), (64, 300, 40),
+          (127, 129, 65), (128, 128, 64), (129, 257, 72), (130, 200, 136), (257, 511, 320), (300, 1000, 24),
+          (513, 40, 130), (700, 96, 33), (1, 777, 2050), (5, 2048, 4096), (1030, 264, 512)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_linear_matches_oracle(shape, dtype):
+    m, n, k = shape
+    rng = np.random.default_rng(m * 7 + n)
+    x, w = matrix(rng, m, k, dtype), matrix(rng, n, k, dtype, scale=k ** -0.5)
+    b = matrix(rng, 1, n, dtype)[0]
+    st = status()
+    bz = sum_bound(to64(x), to64(w), k)
+    plain = opr.opr_linear(x, w, dev_status=st)
+    assert opr.read_status(st) == []
+    within(plain, to64(x) @ to64(w).T, bz, dtype, f"{shape}")
+    # bias, activation, residual and z together, fp32 out
+    r = matrix(rng, m, n, "fp32")
+    y, z = opr.opr_linear(x, w, b, "silu", r, out_dtype=torch.float32, save_z=True, dev_status=st)
+    assert opr.read_status(st) == []
+    ry, rz = lo.linear(to64(x), to64(w), to64(b), "silu", to64(r))
+    bz = bz + (np.abs(rz) + 1) * 2.0 ** -23
+    within(z, rz, bz, dtype, f"z {shape}")
+    within(y, ry, act_bound(rz, bz, "silu") + (np.abs(ry) + np.abs(to64(r))) * 2.0 ** -23, "fp32", f"y {shape}")
+
+
+@pytest.mark.parametrize("activation", [None, "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("types", [("bf16", "bf16", "bf16", "bf16"), ("fp16", "fp32", "bf16", "fp16"),
+                                   ("bf16", "fp16", "fp32", "fp32"), ("fp16", None, "fp16", "bf16"),
+                                   ("bf16", "bf16", None, "fp16")])
+def test_linear_epilogues(types, activation):
+    dtype, bt, rt, yt = types
+    rng = np.random.default_rng(3)
+    for m, n, k in ((37, 100, 80), (200, 264, 128)):
+        x, w = matrix(rng, m, k, dtype), matrix(rng, n, k, dtype, scale=2 * k ** -0.5)
+        b = matrix(rng, 1, n, bt)[0] if bt else None
+        r = matrix(rng, m, n, rt) if rt else None
+        y = opr.opr_linear(x, w, b, activation, r, out_dtype=TYPES[yt])
+        ry, rz = lo.linear(to64(x), to64(w), 0 if b is None else to64(b), activation, None if r is None else to64(r))
+        bz = sum_bound(to64(x), to64(w), k) + (np.abs(rz) + 2) * 2.0 ** -23
+        within(y, ry, act_bound(rz, bz, activation) + (np.abs(ry) + 4) * 2.0 ** -23, yt, f"{m, n, k}")
+
+
+@pytest.mark.parametrize("wide,offset", [(8, 0), (8, 8), (64, 16), (3, 0), (8, 1)])
+def test_linear_on_parts_of_wider_rows(wide, offset):
+    """Operands, residual and result inside wider rows, on and off the 16-byte grid; nothing else is written,
+    and what lies next to the operands does not reach the sums (it is NaN here)."""
+    rng = np.random.default_rng(4)
+    m, n, k = 150, 72, 104
+
+    def inside(rows, cols, dtype):
+        t = torch.full((rows + 2, cols + wide), float("nan"), dtype=TYPES[dtype], device="cuda")
+        v = t[1:rows + 1, offset:offset + cols]
+        v.copy_(matrix(rng, rows, cols, dtype))
+        return t, v
+
+    (_, x), (_, w), (_, r) = inside(m, k, "bf16"), inside(n, k, "bf16"), inside(m, n, "bf16")
+    ty, y = inside(m, n, "bf16")
+    ty.fill_(5.0)
+    got = opr.opr_linear(x, w, residual=r, out=y)
+    ref = to64(x) @ to64(w).T + to64(r)
+    within(got, ref, sum_bound(to64(x), to64(w), k) + np.abs(ref) * 2.0 ** -23, "bf16")
+    rest = torch.ones_like(ty, dtype=torch.bool)
+    rest[1:m + 1, offset:offset + n] = False
+    assert (ty[rest] == 5).all()
+    # gradients of the same views, into views
+    dy = matrix(rng, m, n, "bf16")
+    (tdx, dx), (tdw, dw) = inside(m, k, "bf16"), inside(n, k, "bf16")
+    tdx.fill_(5.0), tdw.fill_(5.0)
+    opr.opr_linear_bwd(dy, x, w, out=(dx, dw))
+    within(dx, to64(dy) @ to64(w), sum_bound(to64(dy), to64(w).T, n), "bf16")
+    within(dw, to64(dy).T @ to64(x), sum_bound(to64(dy).T, to64(x).T, m), "bf16")
+    for t, rows, cols in ((tdx, m, k), (tdw, n, k)):
+        rest = torch.ones_like(t, dtype=torch.bool)
+        rest[1:rows + 1, offset:offset + cols] = False
+        assert (t[rest] == 5).all()
+
+
+def test_linear_into_its_residual():
+    rng = np.random.default_rng(5)
+    x, w, r = matrix(rng, 300, 128, "bf16"), matrix(rng, 200, 128, "bf16"), matrix(rng, 300, 200, "fp32")
+    want = opr.opr_linear(x, w, residual=r, out_dtype=torch.float32)
+    got = opr.opr_linear(x, w, residual=r, out=r)
+    assert got is r and torch.equal(got, want)
+    dy, add = matrix(rng, 300, 200, "bf16"), matrix(rng, 300, 128, "bf16")
+    want, _, _ = opr.opr_linear_bwd(dy, x, w, dx_residual=add, need_dw=False)
+    got, dw, db = opr.opr_linear_bwd(dy, x, w, dx_residual=add, need_dw=False, out=(add, None))
+    assert got is add and dw is None and db is None and torch.equal(got, want)
+
+
+def test_linear_keeps_infinities_and_nan_in_their_rows():
+    rng = np.random.default_rng(6)
+    x, w = matrix(rng, 140, 64, "bf16"), matrix(rng, 96, 64, "bf16")
+    clean = opr.opr_linear(x, w)
+    x[3, 5], x[139, 0] = float("inf"), float("nan")
+    y = opr.opr_linear(x, w)
+    rows = torch.ones(140, dtype=torch.bool, device="cuda")
+    rows[[3, 139]] = False
+    assert torch.equal(y[rows], clean[rows]) and y[139].isnan().all() and not y[3].isfinite().any()
+
+
+def test_linear_flags_fp16_overflow():
+    st = status()
+    x, w = torch.full((4, 64), 64.0, dtype=torch.float16, device="cuda"), torch.ones(8, 64, dtype=torch.float16, device="cuda")
+    opr.opr_linear(x, w, dev_status=st)
+    assert opr.read_status(st) == []
+    opr.opr_linear(x, w * 16, dev_status=st)  # 65536
+    assert opr.read_status(st) == [_abi.DEV_BITS[16]]
+    y = opr.opr_linear(x, w * 16, out_dtype=torch.float32, dev_status=st.zero_())
+    assert opr.read_status(st) == [] and (y == 65536).all()
+
+
+BWD_SHAPES = [(1, 8, 8), (1, 1, 1), (3, 130, 7), (64, 64, 64), (129, 72, 200), (300, 257, 96), (1000, 40, 264),
+              (2500, 96, 128), (130, 513, 33), (17, 2000, 1024), (5000, 136, 72)]
+
+
+@pytest.mark.parametrize("activation", [None, "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("shape", BWD_SHAPES, ids=str)
+def test_linear_gradients_match_oracle(shape, dtype, activation):
+    """With an activation dz is rounded for the products: half a step of each |dz|, times the other factor,
+    summed (the worst case), and the whole dx and dw within one step (two independent half steps) in norm."""
+    m, n, k = shape
+    rng = np.random.default_rng(m + 3 * n)
+    x, w, dy = matrix(rng, m, k, dtype), matrix(rng, n, k, dtype, scale=k ** -0.5), matrix(rng, m, n, dtype)
+    z = matrix(rng, m, n, dtype, scale=2.0) if activation else None
+    add = matrix(rng, m, k, dtype)
+    st = status()
+    dx, dw, db = opr.opr_linear_bwd(dy, x, w, z, activation, dx_residual=add, bias=True, dev_status=st)
+    assert opr.read_status(st) == []
+    X, W = to64(x), to64(w)
+    rx, rw, rb, dz = lo.linear_bwd(to64(dy), X, W, to64(z) if activation else None, activation, to64(add))
+    # the slope in fp32 within 2^-19 (its terms are at most a few units), dz rounded to the operands' type
+    slip = 0 * dz if activation is None else np.abs(to64(dy)) * 2.0 ** -19
+    off = slip if activation is None else slip + half_step(dtype) * (np.abs(dz) + slip) + (2.0 ** -25 if dtype == "fp16" else 0)
+    within(dx, rx, sum_bound(dz, W.T, n) + off @ np.abs(W) + np.abs(rx) * 2.0 ** -23, dtype, f"dx {shape}")
+    within(dw, rw, sum_bound(dz.T, X.T, m) + off.T @ np.abs(X), dtype, f"dw {shape}")
+    # db: a chain of at most 1024 fp32 additions
+    within(db, rb, np.abs(dz).sum(0) * 2.0 ** -14 + slip.sum(0), "fp32", f"db {shape}")
+    eps = torch.finfo(TYPES[dtype]).eps
+    for got, ref in ((dx, rx), (dw, rw)):
+        assert np.linalg.norm(to64(got) - ref) <= eps * np.linalg.norm(ref)
+    # each result asked for alone is the same, bit for bit
+    a, none, no = opr.opr_linear_bwd(dy, x, w, z, activation, dx_residual=add, need_dw=False)
+    assert none is None and no is None and torch.equal(a, dx)
+    _, b, _ = opr.opr_linear_bwd(dy, x, w, z, activation, need_dx=False)
+    _, _, c = opr.opr_linear_bwd(dy, x, w, z, activation, bias=True, need_dx=False, need_dw=False)
+    assert torch.equal(b, dw) and torch.equal(c, db)
+
+
+def test_linear_gradients_in_fp32():
+    rng = np.random.default_rng(8)
+    m, n, k = 3000, 136, 200
+    x, w, dy = matrix(rng, m, k, "bf16"), matrix(rng, n, k, "bf16"), matrix(rng, m, n, "bf16")
+    dx, dw, _ = opr.opr_linear_bwd(dy, x, w, dx_dtype=torch.float32, dw_dtype=torch.float32)
+    within(dx, to64(dy) @ to64(w), sum_bound(to64(dy), to64(w).T, n), "fp32")
+    within(dw, to64(dy).T @ to64(x), sum_bound(to64(dy).T, to64(x).T, m), "fp32")
+
+
+def test_linear_of_no_rows():
+    x, w = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(40, 64, dtype=torch.bfloat16, device="cuda")
+    assert opr.opr_linear(x, w).shape == (0, 40)
+    dx, dw, db = opr.opr_linear_bwd(torch.empty(0, 40, dtype=torch.bfloat16, device="cuda"), x, w, bias=True)
+    assert dx.shape == (0, 64) and (dw == 0).all() and (db == 0).all() and dw.shape == (40, 64)
+
+
+def test_linear_refusals_of_tensors():
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(x=x.float()), dict(w=w.half()), dict(w=w[:, :32]), dict(x=x.t()), dict(bias=x[0]),
+                dict(activation="relu6"), dict(residual=x), dict(out=torch.zeros(4, 9, device="cuda")),
+                dict(out_dtype=torch.float64), dict(dev_status=torch.zeros(1, device="cuda")), dict(out=x[:, :8])):
+        with pytest.raises(opr.OprError):
+            opr.opr_linear(**{**dict(x=x, w=w), **bad})
+    dy = torch.zeros(4, 8, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(dy=dy.float()), dict(dy=dy[:3]), dict(activation="silu"), dict(need_dx=False, dx_residual=x),
+                dict(out=(x, None)), dict(out=(None, w)), dict(dw_dtype=torch.int32)):
+        with pytest.raises(opr.OprError):
+            opr.opr_linear_bwd(**{**dict(dy=dy, x=x, w=w), **bad})
+
+
+@pytest.mark.parametrize("sizes", [(150, 136, 264), (37, 65, 33), (1, 1024, 512)], ids=str)
+def test_linear_on_a_side_stream_and_in_a_graph(sizes):
+    m, n, k = sizes
+    rng = np.random.default_rng(9)
+    x, w, dy = matrix(rng, m, k, "bf16"), matrix(rng, n, k, "bf16"), matrix(rng, m, n, "bf16")
+
+    def step():
+        y, z = opr.opr_linear(x, w, activation="gelu_tanh", save_z=True)
+        return (y, z, *opr.opr_linear_bwd(dy, x, w, z, "gelu_tanh", bias=True))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        first = step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, held))
+    x.copy_(matrix(rng, m, k, "bf16"))
+    graph.replay()
+    with torch.cuda.stream(side):
+        other = step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, held))
