@@ -96,21 +96,37 @@ opr_status map_fail() {
   return OPR_CUDA_ERROR;
 }
 
+}  // namespace
+
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, void* p, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* elem_strides,
+                  CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  return fn != nullptr &&
+         fn(map, type, static_cast<cuuint32_t>(rank), p, dims, strides, box, elem_strides,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint32_t wait_limit_ns() {
+  const uint64_t limit = g_wait_limit_ns.load();
+  return limit > 0xFFFFFFFFull ? 0xFFFFFFFFu : static_cast<uint32_t>(limit);
+}
+
+namespace {
+
 // [tokens, heads, head_dim] 16-bit tensor (bf16 or fp16) as a 3-D TMA map with
 // 128-byte swizzle; a box is 64 head_dim elements x 1 head x 128 tokens (rows
 // past the end read 0).
 bool make_map(CUtensorMap* map, const void* ptr, int64_t total, int32_t heads, int32_t head_dim,
               bool f16 = false) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
                         static_cast<cuuint64_t>(total)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(heads) * head_dim * 2};
   cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(kTile)};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                      const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -139,8 +155,7 @@ AttnParams base_params(const int32_t* cu_seqlens, const int32_t* conv_idx, const
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.dev_status = dev_status;
-  const uint64_t limit = g_wait_limit_ns.load();
-  p.wait_ns = limit > 0xFFFFFFFFull ? 0xFFFFFFFFu : static_cast<uint32_t>(limit);
+  p.wait_ns = wait_limit_ns();
   return p;
 }
 

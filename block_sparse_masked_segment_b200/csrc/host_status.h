@@ -21,6 +21,15 @@ inline opr_status status_of(cudaError_t e) { return e == cudaSuccess ? OPR_OK : 
 // OPR_UNSUPPORTED unless the current device has compute capability 10.x (defined in api.cu).
 opr_status device_check();
 
+// Limit of the kernels' pipeline waits, as AttnParams::wait_ns (defined in api.cu).
+uint32_t wait_limit_ns();
+
+// Encodes a tiled TMA map with interleave off, 256-byte L2 promotion and zeros out
+// of bounds; false when the driver refuses it (defined in api.cu).
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, void* p, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* elem_strides,
+                  CUtensorMapSwizzle swizzle);
+
 // Host check of the sizes shared by the layout and attention calls: non-negative,
 // int32 token offsets, and total tokens within n_seqs * ceil(max_seqlen / 128) * 128,
 // the bound the workspaces are sized by (defined in api.cu).

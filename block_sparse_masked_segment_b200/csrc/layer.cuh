@@ -117,6 +117,9 @@ struct Operand {
 
 cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t m, int32_t n, int64_t k, int32_t dtype,
                           const LinearEpilogue& e, int32_t* dev_status, cudaStream_t stream);
+// Both operands' rows (columns, where `col` is the row length) start on 16-byte boundaries.
+// Copies a 16-bit matrix to rows of `ld` entries.
+cudaError_t launch_pack(const Operand& from, int64_t rows, int64_t cols, void* to, int64_t ld, cudaStream_t stream);
 cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int64_t ldz, int32_t dtype, int64_t m,
                              int32_t n, int32_t activation, void* dz, int64_t ld_dz, float* db, float* partial,
                              int32_t* dev_status, cudaStream_t stream);

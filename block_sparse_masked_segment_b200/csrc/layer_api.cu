@@ -93,6 +93,13 @@ size_t copy_bytes(int64_t rows, int64_t cols) {
   return align_up(static_cast<size_t>(rows) * static_cast<size_t>(padded(cols)) * 2, 256);
 }
 
+// Copies an operand's rows to `to` with padded rows and points the operand there.
+cudaError_t pack(Operand& o, int64_t rows, int64_t cols, void* to, cudaStream_t stream) {
+  const cudaError_t e = launch_pack(o, rows, cols, to, padded(cols), stream);
+  o = Operand{to, padded(cols), 1};
+  return e;
+}
+
 bool linear_sizes_ok(int64_t m, int32_t n, int32_t k) { return m >= 0 && m < kMaxRows && n > 0 && k > 0; }
 bool known_act(int32_t a) { return a >= OPR_ACT_NONE && a <= OPR_ACT_GELU_TANH; }
 
@@ -343,11 +350,19 @@ opr_status opr_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
                           {{z, m, ldz, n, dtype}, {nullptr, nullptr}},
                           {{workspace, 1, ws_words, ws_words, OPR_DTYPE_FP32}, {nullptr, nullptr}}};
   if (outputs_clash(in, out)) return OPR_INVALID_ARG;
-  const opr_status st = device_check();
+  opr_status st = device_check();
+  if (st != OPR_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Operand ox{x, ldx, 1}, ow{w, ldw, 1};
+  char* to = static_cast<char*>(workspace);
+  if (!tma_ready(x, ldx)) {
+    st = status_of(pack(ox, m, k, to, s));
+    to += copy_bytes(m, k);
+  }
+  if (st == OPR_OK && !tma_ready(w, ldw)) st = status_of(pack(ow, n, k, to, s));
   if (st != OPR_OK) return st;
   LinearEpilogue e{bias, bias_dtype, activation, residual, ld_residual, residual_dtype, y, ldy, y_dtype, z, ldz};
-  return status_of(launch_linear(Operand{x, ldx, 1}, Operand{w, ldw, 1}, m, n, k, dtype, e, dev_status,
-                                 static_cast<cudaStream_t>(stream)));
+  return status_of(launch_linear(ox, ow, m, n, k, dtype, e, dev_status, s));
 }
 
 namespace {
@@ -428,6 +443,10 @@ opr_status opr_linear_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t 
                                     db, reinterpret_cast<float*>(wsp + ws.partial), dev_status, s));
     if (st != OPR_OK) return st;
   }
+  Operand ox{x, ldx, 1}, ow{w, ldw, 1};
+  if (dw && m > 0 && !tma_ready(x, ldx)) st = status_of(pack(ox, m, k, wsp + ws.x, s));
+  if (st == OPR_OK && dx && m > 0 && !tma_ready(w, ldw)) st = status_of(pack(ow, n, k, wsp + ws.w, s));
+  if (st != OPR_OK) return st;
   if (dx) {
     LinearEpilogue e{};
     e.residual = dx_residual;
@@ -436,7 +455,7 @@ opr_status opr_linear_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t 
     e.y = dx;
     e.ldy = ld_dx;
     e.y_dtype = dx_dtype;
-    st = status_of(launch_linear(Operand{dz, ld_dz, 1}, Operand{w, 1, ldw}, m, k, n, dtype, e, dev_status, s));
+    st = status_of(launch_linear(Operand{dz, ld_dz, 1}, Operand{ow.p, 1, ow.row}, m, k, n, dtype, e, dev_status, s));
     if (st != OPR_OK) return st;
   }
   if (dw) {
@@ -444,7 +463,7 @@ opr_status opr_linear_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t 
     e.y = dw;
     e.ldy = ld_dw;
     e.y_dtype = dw_dtype;
-    st = status_of(launch_linear(Operand{dz, 1, ld_dz}, Operand{x, 1, ldx}, n, k, m, dtype, e, dev_status, s));
+    st = status_of(launch_linear(Operand{dz, 1, ld_dz}, Operand{ox.p, 1, ox.row}, n, k, m, dtype, e, dev_status, s));
   }
   return st;
 }

@@ -5,6 +5,8 @@
 // 16-bit operands, fp32 sums, each output rounded once.
 #include <algorithm>
 
+#include "attn_common.cuh"
+#include "host_status.h"
 #include "layer.cuh"
 
 namespace opr {
@@ -48,52 +50,234 @@ __device__ __forceinline__ bool store_typed(void* p, int32_t dtype, int64_t i, f
   return false;
 }
 
-constexpr int kEdge = 64, kDepth = 16;
+// ---------------------------------------------------------------- tiles
+// A product is C(p, q) = sum_k P(p, k) Q(q, k): P fills the 128 rows (TMEM lanes)
+// of a tile, Q its BN columns.  An operand is K-major (k contiguous) or MN-major
+// (its rows contiguous); a 64-deep slice of R rows is staged as
+//   K-major   R rows of 128 bytes (64 k), one box
+//   MN-major  R / 64 chunks of 64 k-rows of 128 bytes (64 rows of the operand)
+// with the 128-byte swizzle.  Boxes past the ends read zeros.
+constexpr int kRowsP = 128;
+constexpr int kDepth = 64;
+constexpr int kChunk = kDepth * 128;  // bytes of an MN-major chunk
 
-// One 64 x 64 tile per block of 256 threads, 4 x 4 outputs a thread, fp32 sums.
-template <typename T>
-__global__ void __launch_bounds__(256) linear_kernel(const Operand a, const Operand b, int64_t m, int32_t n, int64_t k,
-                                                     int32_t dtype, const LinearEpilogue e, int32_t* dev_status) {
-  __shared__ float as[kDepth][kEdge + 1], bs[kDepth][kEdge + 1];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kEdge;
-  const int64_t j0 = static_cast<int64_t>(blockIdx.y) * kEdge;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const T *pa = static_cast<const T*>(a.p), *pb = static_cast<const T*>(b.p);
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < k; k0 += kDepth) {
-    for (int t = threadIdx.x; t < kEdge * kDepth; t += 256) {
-      // neighbouring threads along the operand's contiguous direction
-      const int ra = a.col == 1 ? t / kDepth : t % kEdge, ka = a.col == 1 ? t % kDepth : t / kEdge;
-      as[ka][ra] = i0 + ra < m && k0 + ka < k ? as_float(pa[(i0 + ra) * a.row + (k0 + ka) * a.col]) : 0.f;
-      const int rb = b.col == 1 ? t / kDepth : t % kEdge, kb = b.col == 1 ? t % kDepth : t / kEdge;
-      bs[kb][rb] = j0 + rb < n && k0 + kb < k ? as_float(pb[(j0 + rb) * b.row + (k0 + kb) * b.col]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kDepth; ++kk) {
-      float av[4], bv[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) av[q] = as[kk][ty + 16 * q], bv[q] = bs[kk][tx + 16 * q];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[q][r] = fmaf(av[q], bv[r], acc[q][r]);
-    }
-    __syncthreads();
+template <bool MN>
+__device__ __forceinline__ void load_slice(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int row0, int k0,
+                                           int rows) {
+  auto box = [&](uint8_t* to, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(to)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+  };
+  if constexpr (MN) {
+    for (int c = 0; c < rows / 64; ++c) box(dst + c * kChunk, row0 + 64 * c, k0);
+  } else {
+    box(dst, k0, row0);
   }
+}
+
+// Descriptor of a staged slice, and its step from 16 k to the next 16 k.
+template <bool MN>
+__device__ __forceinline__ uint64_t slice_desc(uint32_t saddr) {
+  return MN ? smem_desc_sw128(saddr, kChunk, 1024) : smem_desc_sw128(saddr, 16, 1024);
+}
+template <bool MN>
+__device__ __forceinline__ constexpr uint64_t slice_step(int kk) {
+  return static_cast<uint64_t>((MN ? kk * 2048 : kk * 32) >> 4);
+}
+
+struct ProductArgs {
+  int64_t rows_p;
+  int32_t rows_q;
+  int64_t depth;
+  int32_t f16;
+  int32_t tiles_p, tiles_q;
+  LinearEpilogue e;
+  int32_t* dev_status;
+  uint32_t wait_ns;
+};
+
+// One output: bias, z, activation, residual, rounding.  Returns whether an fp16
+// value overflowed.
+__device__ __forceinline__ bool finish(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, float z) {
   bool bad = false;
-  for (int q = 0; q < 4; ++q)
-    for (int r = 0; r < 4; ++r) {
-      const int64_t i = i0 + ty + 16 * q, j = j0 + tx + 16 * r;
-      if (i >= m || j >= n) continue;
-      float z = acc[q][r];
-      if (e.bias != nullptr) z += load_typed(e.bias, e.bias_dtype, j);
-      if (e.z != nullptr) bad |= store_typed(e.z, dtype, i * e.ldz + j, z);
-      z = activate(z, e.activation);
-      if (e.residual != nullptr) z += load_typed(e.residual, e.residual_dtype, i * e.ld_residual + j);
-      bad |= store_typed(e.y, e.y_dtype, i * e.ldy + j, z);
+  if (e.bias != nullptr) z += load_typed(e.bias, e.bias_dtype, n);
+  if (e.z != nullptr) bad |= store_typed(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, z);
+  z = activate(z, e.activation);
+  if (e.residual != nullptr) z += load_typed(e.residual, e.residual_dtype, m * e.ld_residual + n);
+  return store_typed(e.y, e.y_dtype, m * e.ldy + n, z) || bad;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float load_peer(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+constexpr int kProductThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
+constexpr int kProductSmem = 225 * 1024;
+
+template <int BN>
+struct TileSmem {
+  static constexpr int kStageBytes = kRowsP * 128 + (BN < 64 ? 64 : BN) * 128;
+  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  alignas(1024) uint8_t ring[kStages][kStageBytes];
+  uint64_t full[kStages], empty[kStages], done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// One 128 x BN tile per cluster, its depth split over the cluster's CTAs.  Each CTA
+// leaves its partial tile (fp32) in its own shared memory, where the ring was; after
+// the cluster's barrier each CTA adds up and finishes every cluster-size-th line of
+// the tile, the partials in rank order (deterministic, no workspace, one launch).
+// SWAP: the lines of C are columns of y (P holds the n side, Q the m side).
+template <bool P_MN, bool Q_MN, int BN, bool SWAP>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    product_tile_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ ProductArgs a) {
+  using Smem = TileSmem<BN>;
+  constexpr int kStages = Smem::kStages;
+  constexpr uint32_t kCols = BN < 32 ? 32 : BN;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(align1024(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x / ranks) * kRowsP;
+  const int q0 = blockIdx.y * BN;
+  const int64_t slices = (a.depth + kDepth - 1) / kDepth;
+  const int s0 = static_cast<int>(slices * rank / ranks), s1 = static_cast<int>(slices * (rank + 1) / ranks);
+  const int n = s1 - s0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
     }
-  if (bad && dev_status != nullptr) atomicOr(dev_status, OPR_DEV_FP16_RANGE);
+    mbar_init(&sm.done, 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort_flag = &sm.abort_flag;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      constexpr int kRowsQ = Q_MN && BN < 64 ? 64 : BN;  // an MN-major chunk has 64 rows
+      constexpr uint32_t kBytes = (kRowsP + kRowsQ) * 128;
+      int issued = 0;
+      for (int j = 0; j < n; ++j) {
+        const int s = j % kStages;
+        if (j >= kStages && !mbar_wait(&sm.empty[s], ((j / kStages) + 1) & 1, abort_flag, a.wait_ns)) break;
+        mbar_arrive_expect_tx(&sm.full[s], kBytes);
+        load_slice<P_MN>(&map_p, &sm.full[s], sm.ring[s], static_cast<int>(p0), (s0 + j) * kDepth, kRowsP);
+        load_slice<Q_MN>(&map_q, &sm.full[s], sm.ring[s] + kRowsP * 128, q0, (s0 + j) * kDepth, kRowsQ);
+        issued = j + 1;
+      }
+      // every copy issued has landed before the CTA goes on (also after an abort)
+      for (int j = (issued > kStages ? issued - kStages : 0); j < issued; ++j)
+        mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, nullptr, kWaitLimitNs);
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f32acc(kRowsP, BN, a.f16 != 0, P_MN, Q_MN);
+    for (int j = 0; j < n; ++j) {
+      const int s = j % kStages;
+      if (!warp_wait(&sm.full[s], (j / kStages) & 1, abort_flag, a.wait_ns)) break;
+      tc_fence_after();
+      const uint32_t sa = smem_u32(sm.ring[s]);
+      const uint64_t dp = slice_desc<P_MN>(sa), dq = slice_desc<Q_MN>(sa + kRowsP * 128);
+#pragma unroll
+      for (int kk = 0; kk < kDepth / 16; ++kk)
+        mma_ss(tmem, dp + slice_step<P_MN>(kk), dq + slice_step<Q_MN>(kk), idesc, (j | kk) != 0 ? 1u : 0u);
+      mma_commit(&sm.empty[s]);
+    }
+    mma_commit(&sm.done);
+    __all_sync(0xffffffffu, mbar_wait(&sm.done, 0, nullptr, kWaitLimitNs));
+  }
+  // the partial tile: [128][BN + 1] (lines along q) or, swapped, [BN][128] (lines along p)
+  float* part = reinterpret_cast<float*>(sm.ring);
+  const bool ok = mbar_wait(&sm.done, 0, nullptr, kWaitLimitNs);
+  __syncthreads();
+  const bool aborted = *abort_flag != 0 || !ok;
+  tc_fence_after();
+  if (warp >= 2) {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int row = quad * 32 + lane;
+    for (int c = half * 16; c < BN; c += 32) {
+      uint32_t r[16];
+      tmem_ld16(tl + c, r);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float v = n > 0 ? __uint_as_float(r[i]) : 0.f;
+        if constexpr (SWAP)
+          part[(c + i) * kRowsP + row] = v;
+        else
+          part[row * (BN + 1) + c + i] = v;
+      }
+    }
+    tc_fence_before();
+  }
+  cluster_sync();
+  bool bad = false;
+  const uint32_t base = smem_u32(part);
+  if constexpr (SWAP) {
+    const int lines = a.rows_q - q0 < BN ? a.rows_q - q0 : BN;
+    for (int i = static_cast<int>(rank) + static_cast<int>(ranks) * (threadIdx.x / kRowsP); i < lines;
+         i += static_cast<int>(ranks) * 2) {
+      if (threadIdx.x >= 2 * kRowsP) break;
+      const int p = threadIdx.x % kRowsP;
+      if (p0 + p >= a.rows_p) continue;
+      float v = 0.f;
+      for (uint32_t r = 0; r < ranks; ++r) v += load_peer(base + 4 * (i * kRowsP + p), r);
+      bad |= finish(a.e, a.f16 != 0, q0 + i, p0 + p, v);
+    }
+  } else {
+    const int lines = a.rows_p - p0 < kRowsP ? static_cast<int>(a.rows_p - p0) : kRowsP;
+    for (int i = static_cast<int>(rank) + static_cast<int>(ranks) * warp; i < lines;
+         i += static_cast<int>(ranks) * (kProductThreads / 32)) {
+      for (int c = lane; c < BN; c += 32) {
+        if (q0 + c >= a.rows_q) continue;
+        float v = 0.f;
+        for (uint32_t r = 0; r < ranks; ++r) v += load_peer(base + 4 * (i * (BN + 1) + c), r);
+        bad |= finish(a.e, a.f16 != 0, p0 + i, q0 + c, v);
+      }
+    }
+  }
+  if (bad) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
+  if (aborted && threadIdx.x == 0) atomicOr(a.dev_status, OPR_DEV_WAIT_TIMEOUT);
+  cluster_sync();  // no CTA ends while another reads its shared memory
+  if (warp == 1) tmem_dealloc(tmem, kCols);
+}
+
+// A matrix whose rows start off the 16-byte grid, copied to rows that start on it.
+__global__ void __launch_bounds__(256) pack_kernel(const uint16_t* __restrict__ x, int64_t ldx, int64_t rows,
+                                                   int64_t cols, uint16_t* __restrict__ y, int64_t ldy) {
+  const int64_t n = rows * cols;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    y[i / cols * ldy + i % cols] = x[i / cols * ldx + i % cols];
 }
 
 constexpr int kDzRows = 64;
@@ -134,14 +318,88 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, i
 
 }  // namespace
 
+namespace {
+
+// A 16-bit operand as a 2-D map of boxes of `box_rows` rows of 64 entries along its
+// contiguous direction, 128-byte swizzle.
+bool operand_map(CUtensorMap* map, const Operand& o, int64_t rows, int64_t depth, bool f16, int box_rows) {
+  const bool mn = o.col != 1;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(mn ? rows : depth), static_cast<cuuint64_t>(mn ? depth : rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(mn ? o.col : o.row) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(mn ? kDepth : box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode_tiled(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                      const_cast<void*>(o.p), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool P_MN, bool Q_MN, int BN, bool SWAP>
+cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, int split, cudaStream_t stream) {
+  CUtensorMap mp, mq;
+  // with nothing to add up no box is loaded, and the maps (of valid extents) are not used
+  const int64_t depth = a.depth > 0 ? a.depth : 1;
+  if (!operand_map(&mp, p, a.rows_p, depth, a.f16 != 0, kRowsP) ||
+      !operand_map(&mq, q, a.rows_q, depth, a.f16 != 0, BN))
+    return cudaErrorInvalidValue;
+  auto* kernel = product_tile_kernel<P_MN, Q_MN, BN, SWAP>;
+  static_assert(sizeof(TileSmem<BN>) + 1024 <= kProductSmem, "a tile's ring fits an SM");
+  static_assert((SWAP ? BN * kRowsP : kRowsP * (BN + 1)) * 4 <= static_cast<int>(sizeof(TileSmem<BN>::ring)),
+                "the partial tile fits where the ring was");
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.tiles_p * split), static_cast<unsigned>(a.tiles_q));
+  cfg.blockDim = dim3(kProductThreads);
+  cfg.dynamicSmemBytes = kProductSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mp, mq, a);
+}
+
+template <bool P_MN, bool Q_MN>
+cudaError_t launch_product(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
+  const int64_t slices = (a.depth + kDepth - 1) / kDepth;
+  auto tiles = [&](int bn) { return (a.rows_p + kRowsP - 1) / kRowsP * ((a.rows_q + bn - 1) / bn); };
+  auto go = [&](auto bn) {
+    constexpr int BN = decltype(bn)::value;
+    a.tiles_p = static_cast<int32_t>((a.rows_p + kRowsP - 1) / kRowsP);
+    a.tiles_q = (a.rows_q + BN - 1) / BN;
+    int split = 1;
+    while (split < 8 && tiles(BN) * split * 2 <= 148 && slices >= split * 2 * 4) split *= 2;
+    return launch_tiles<P_MN, Q_MN, BN, false>(p, q, a, split, stream);
+  };
+  if (tiles(256) >= 148) return go(std::integral_constant<int, 256>{});
+  if (tiles(128) >= 148) return go(std::integral_constant<int, 128>{});
+  return go(std::integral_constant<int, 64>{});
+}
+
+}  // namespace
+
 cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t m, int32_t n, int64_t k, int32_t dtype,
                           const LinearEpilogue& e, int32_t* dev_status, cudaStream_t stream) {
   if (m == 0 || n == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((m + kEdge - 1) / kEdge), static_cast<unsigned>((n + kEdge - 1) / kEdge));
-  if (dtype == OPR_DTYPE_BF16)
-    linear_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, b, m, n, k, dtype, e, dev_status);
-  else
-    linear_kernel<__half><<<grid, 256, 0, stream>>>(a, b, m, n, k, dtype, e, dev_status);
+  ProductArgs args{};
+  args.rows_p = m;
+  args.rows_q = n;
+  args.depth = k;
+  args.f16 = dtype == OPR_DTYPE_FP16;
+  args.e = e;
+  args.dev_status = dev_status;
+  args.wait_ns = wait_limit_ns();
+  const bool a_mn = a.col != 1, b_mn = b.col != 1;
+  if (!a_mn && !b_mn) return launch_product<false, false>(a, b, args, stream);
+  if (!a_mn) return launch_product<false, true>(a, b, args, stream);
+  return launch_product<true, true>(a, b, args, stream);
+}
+
+cudaError_t launch_pack(const Operand& from, int64_t rows, int64_t cols, void* to, int64_t ld, cudaStream_t stream) {
+  if (rows == 0) return cudaSuccess;
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((rows * cols + 2047) / 2048, 148 * 16));
+  pack_kernel<<<blocks, 256, 0, stream>>>(static_cast<const uint16_t*>(from.p), from.row, rows, cols,
+                                          static_cast<uint16_t*>(to), ld);
   return cudaGetLastError();
 }
 
