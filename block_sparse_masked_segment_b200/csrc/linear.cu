@@ -94,6 +94,7 @@ struct ProductArgs {
   int64_t depth;
   int32_t f16;
   int32_t tiles_p, tiles_q;
+  int32_t vec;  // y, z, residual and bias allow 16-byte accesses of eight neighbours
   LinearEpilogue e;
   int32_t* dev_status;
   uint32_t wait_ns;
@@ -129,6 +130,12 @@ __device__ __forceinline__ float load_peer(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
+}
+
+// Limit of a wait for a whole tile: 2 us a slice (six times what one takes) on top of
+// the limit of a single wait; 0 stays 0.
+__device__ __forceinline__ uint64_t depth_limit(uint64_t wait_ns, int slices) {
+  return wait_ns == 0 ? 0 : wait_ns + 2000ull * static_cast<uint64_t>(slices);
 }
 
 constexpr int kProductThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   }
   // the partial tile: [128][BN + 1] (lines along q) or, swapped, [BN][128] (lines along p)
   float* part = reinterpret_cast<float*>(sm.ring);
-  const bool ok = mbar_wait(&sm.done, 0, nullptr, kWaitLimitNs);
+  const bool ok = mbar_wait(&sm.done, 0, nullptr, depth_limit(kWaitLimitNs, n));
   __syncthreads();
   const bool aborted = *abort_flag != 0 || !ok;
   tc_fence_after();
@@ -269,6 +276,331 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (aborted && threadIdx.x == 0) atomicOr(a.dev_status, OPR_DEV_WAIT_TIMEOUT);
   cluster_sync();  // no CTA ends while another reads its shared memory
   if (warp == 1) tmem_dealloc(tmem, kCols);
+}
+
+// ---------------------------------------------------------------- large products
+// Persistent CTA pairs: one 256 x 256 tile at a time per pair (cta_group::2), each
+// CTA staging its own 128 rows of P and its half of Q's 256 rows, so that a pair
+// reads each staged byte once where two CTAs of their own would read Q twice.  Two
+// accumulators: the epilogue of a tile runs while the next one is multiplied.
+constexpr int kPairStages = 5;
+constexpr int kPairTile = 256;
+constexpr int kEpiWarps = 8;
+constexpr int kStageLd = 36;  // floats from row to row of a warp's 32 x 32 staging: 16-byte accesses without conflicts
+
+struct PairSmem {
+  alignas(1024) uint8_t ring[kPairStages][2 * kRowsP * 128];
+  alignas(16) float stage[kEpiWarps][32 * kStageLd];
+  uint64_t full[kPairStages], empty[kPairStages];  // full: the leader's, counts both CTAs' bytes
+  uint64_t acc_full[2], acc_empty[2];              // acc_empty: the leader's
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int issued;
+};
+static_assert(sizeof(PairSmem) + 1024 <= kProductSmem, "the ring and the staging fit an SM");
+
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+
+// Loads 128 rows of an operand for the pair; `bar` is the leader's barrier (cluster address).
+template <bool MN>
+__device__ __forceinline__ void load_pair_slice(const CUtensorMap* map, uint32_t bar, uint8_t* dst, int row0, int k0) {
+  auto box = [&](uint8_t* to, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(to)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+  };
+  if constexpr (MN) {
+    box(dst, row0, k0);
+    box(dst + kChunk, row0 + 64, k0);
+  } else {
+    box(dst, k0, row0);
+  }
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred E, P;\n\t"
+      "elect.sync _|E, 0xffffffff;\n\t"
+      "setp.ne.b32 P, %4, 0;\n\t"
+      "@E tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, P;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrives on `bar` of both CTAs when the MMAs issued so far are complete.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred E;\n\t"
+      "elect.sync _|E, 0xffffffff;\n\t"
+      "@E tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
+          "r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// Eight neighbours of a row of type dtype (16-byte aligned).
+__device__ __forceinline__ void load8(const void* p, int32_t dtype, int64_t i, float (&v)[8]) {
+  if (dtype == OPR_DTYPE_FP32) {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = f[0], b = f[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    return;
+  }
+  const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (dtype == OPR_DTYPE_BF16) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ bool store8(void* p, int32_t dtype, int64_t i, const float (&v)[8]) {
+  if (dtype == OPR_DTYPE_FP32) {
+    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    f[0] = make_float4(v[0], v[1], v[2], v[3]);
+    f[1] = make_float4(v[4], v[5], v[6], v[7]);
+    return false;
+  }
+  uint4 u;
+  bool bad = false;
+  if (dtype == OPR_DTYPE_BF16) {
+    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  } else {
+    u = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bad |= !(fabsf(v[k]) <= 65504.f);
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = u;
+  return bad;
+}
+
+__device__ __forceinline__ bool finish8(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, float (&v)[8]) {
+  bool bad = false;
+  if (e.bias != nullptr) {
+    float b[8];
+    load8(e.bias, e.bias_dtype, n, b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += b[k];
+  }
+  if (e.z != nullptr) bad |= store8(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, v);
+  if (e.activation != OPR_ACT_NONE) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = activate(v[k], e.activation);
+  }
+  if (e.residual != nullptr) {
+    float r[8];
+    load8(e.residual, e.residual_dtype, m * e.ld_residual + n, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += r[k];
+  }
+  return store8(e.y, e.y_dtype, m * e.ldy + n, v) || bad;
+}
+
+// Tile t of the walk: groups of kGroup tile rows, columns outer inside a group, so
+// that the pairs that run together share rows of P and Q in L2.
+constexpr int kGroup = 8;
+__device__ __forceinline__ void tile_at(int t, int tiles_p, int tiles_q, int& tp, int& tq) {
+  const int per = kGroup * tiles_q;
+  const int g = t / per, r = t % per;
+  const int rows = tiles_p - g * kGroup < kGroup ? tiles_p - g * kGroup : kGroup;
+  tp = g * kGroup + r % rows;
+  tq = r / rows;
+}
+
+template <bool P_MN, bool Q_MN>
+__global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
+    product_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ ProductArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(align1024(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int slices = static_cast<int>((a.depth + kDepth - 1) / kDepth);
+  const int tiles = a.tiles_p * a.tiles_q;
+  const int pairs = gridDim.x / 2, first = blockIdx.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(&sm.done, 1);
+    sm.abort_flag = 0;
+    sm.issued = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are set up
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort_flag = &sm.abort_flag;
+
+  auto fill = [&](int j, int tp, int tq, int slice) {
+    const int s = j % kPairStages;
+    // the leader's barrier counts both CTAs' bytes of the stage
+    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 4 * kRowsP * 128);
+    const uint32_t bar = peer_addr(smem_u32(&sm.full[s]), 0);
+    load_pair_slice<P_MN>(&map_p, bar, sm.ring[s], tp * kPairTile + static_cast<int>(rank) * kRowsP, slice * kDepth);
+    load_pair_slice<Q_MN>(&map_q, bar, sm.ring[s] + kRowsP * 128, tq * kPairTile + static_cast<int>(rank) * kRowsP,
+                          slice * kDepth);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int j = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += pairs) {
+        int tp, tq;
+        tile_at(t, a.tiles_p, a.tiles_q, tp, tq);
+        for (int k = 0; k < slices; ++k, ++j) {
+          if (j >= kPairStages &&
+              !mbar_wait(&sm.empty[j % kPairStages], ((j / kPairStages) + 1) & 1, abort_flag, a.wait_ns)) {
+            ok = false;
+            break;
+          }
+          fill(j, tp, tq, k);
+        }
+      }
+      sm.issued = j;
+      // the releases of the last stages, which the leader's MMAs send here
+      for (int u = j > kPairStages ? j - kPairStages : 0; ok && u < j; ++u)
+        ok = mbar_wait(&sm.empty[u % kPairStages], (u / kPairStages) & 1, abort_flag, a.wait_ns);
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t idesc = idesc_f32acc(kPairTile, kPairTile, a.f16 != 0, P_MN, Q_MN);
+      int j = 0, i = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += pairs, ++i) {
+        const int b = i & 1;
+        if (i >= 2) ok = warp_wait(&sm.acc_empty[b], ((i >> 1) + 1) & 1, abort_flag, a.wait_ns);
+        tc_fence_after();
+        for (int k = 0; ok && k < slices; ++k, ++j) {
+          const int s = j % kPairStages;
+          ok = warp_wait(&sm.full[s], (j / kPairStages) & 1, abort_flag, a.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(sm.ring[s]);
+          const uint64_t dp = slice_desc<P_MN>(sa), dq = slice_desc<Q_MN>(sa + kRowsP * 128);
+#pragma unroll
+          for (int kk = 0; kk < kDepth / 16; ++kk)
+            mma_pair(tmem + b * kPairTile, dp + slice_step<P_MN>(kk), dq + slice_step<Q_MN>(kk), idesc,
+                     (k | kk) != 0 ? 1u : 0u);
+          commit_pair(&sm.empty[s]);
+        }
+        if (ok) commit_pair(&sm.acc_full[b]);
+      }
+      // the releases of the last accumulators, which the peer sends here, and the last MMA
+      for (int u = i > 2 ? i - 2 : 0; ok && u < i; ++u)
+        ok = warp_wait(&sm.acc_empty[u & 1], (u >> 1) & 1, abort_flag, a.wait_ns);
+      asm volatile(
+          "{\n\t.reg .pred E;\n\t"
+          "elect.sync _|E, 0xffffffff;\n\t"
+          "@E tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+              smem_u32(&sm.done))
+          : "memory");
+      __all_sync(0xffffffffu, mbar_wait(&sm.done, 0, nullptr, kWaitLimitNs));
+    }
+  } else {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    float* stage = sm.stage[warp - 2];
+    const LinearEpilogue& e = a.e;
+    const bool f16 = a.f16 != 0;
+    bool bad = false;
+    int i = 0;
+    for (int t = first; t < tiles; t += pairs, ++i) {
+      const int b = i & 1;
+      int tp, tq;
+      tile_at(t, a.tiles_p, a.tiles_q, tp, tq);
+      if (!warp_wait(&sm.acc_full[b], (i >> 1) & 1, abort_flag, depth_limit(a.wait_ns, slices))) break;
+      tc_fence_after();
+      const int64_t m0 = static_cast<int64_t>(tp) * kPairTile + rank * kRowsP + quad * 32;
+      for (int c = 0; c < 4; ++c) {
+        const int col = half * 128 + c * 32;
+        uint32_t r[32];
+        tmem_ld32(tl + b * kPairTile + col, r);
+        if (c == 3) {  // this warp has read its part of the accumulator
+          tc_fence_before();
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                             peer_addr(smem_u32(&sm.acc_empty[b]), 0))
+                         : "memory");
+        }
+        const int64_t n0 = static_cast<int64_t>(tq) * kPairTile + col;
+        if (m0 >= a.rows_p || n0 >= a.rows_q) continue;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<uint4*>(stage + lane * kStageLd + 4 * q) =
+              make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+        __syncwarp();
+        if (a.vec) {
+          const int64_t n = n0 + (lane & 3) * 8;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int row = q * 8 + (lane >> 2);
+            if (m0 + row >= a.rows_p || n >= a.rows_q) continue;
+            float v[8];
+            const float4* f = reinterpret_cast<const float4*>(stage + row * kStageLd + (lane & 3) * 8);
+            const float4 x = f[0], y = f[1];
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+            bad |= finish8(e, f16, m0 + row, n, v);
+          }
+        } else if (n0 + lane < a.rows_q) {
+          for (int row = 0; row < 32 && m0 + row < a.rows_p; ++row)
+            bad |= finish(e, f16, m0 + row, n0 + lane, stage[row * kStageLd + lane]);
+        }
+        __syncwarp();
+      }
+    }
+    if (bad) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
+  }
+  __syncthreads();
+  cluster_sync();
+  // After an abort the two producers may have stopped at different slices: the one
+  // behind catches up (no MMA reads the ring any more), so that the leader's
+  // barriers, which count both, say when every copy of both CTAs has landed.
+  if (threadIdx.x == 0) {
+    const int mine = sm.issued;
+    int theirs;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(theirs) : "r"(peer_addr(smem_u32(&sm.issued), rank ^ 1u)));
+    const int upto = mine > theirs ? mine : theirs;
+    for (int j = mine; j < upto; ++j) fill(j, 0, 0, 0);
+    if (rank == 0)
+      for (int j = upto > kPairStages ? upto - kPairStages : 0; j < upto; ++j)
+        mbar_wait(&sm.full[j % kPairStages], (j / kPairStages) & 1, nullptr, kWaitLimitNs);
+    if (*abort_flag != 0) atomicOr(a.dev_status, OPR_DEV_WAIT_TIMEOUT);
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 // A matrix whose rows start off the 16-byte grid, copied to rows that start on it.
@@ -359,6 +691,28 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, int 
   return cudaLaunchKernelEx(&cfg, kernel, mp, mq, a);
 }
 
+bool vector_epilogue(const LinearEpilogue& e, int32_t n) {
+  auto fits = [](const void* p, int64_t ld) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0); };
+  return n % 8 == 0 && fits(e.y, e.ldy) && fits(e.z, e.ldz) && fits(e.residual, e.ld_residual) && fits(e.bias, 0);
+}
+
+template <bool P_MN, bool Q_MN>
+cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
+  CUtensorMap mp, mq;
+  if (!operand_map(&mp, p, a.rows_p, a.depth, a.f16 != 0, kRowsP) ||
+      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, kRowsP))
+    return cudaErrorInvalidValue;
+  auto* kernel = product_pair_kernel<P_MN, Q_MN>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+  if (e != cudaSuccess) return e;
+  a.tiles_p = static_cast<int32_t>((a.rows_p + kPairTile - 1) / kPairTile);
+  a.tiles_q = (a.rows_q + kPairTile - 1) / kPairTile;
+  a.vec = vector_epilogue(a.e, a.rows_q);
+  const int64_t pairs = std::min<int64_t>(static_cast<int64_t>(a.tiles_p) * a.tiles_q, 148 / 2);
+  kernel<<<static_cast<unsigned>(2 * pairs), kProductThreads, kProductSmem, stream>>>(mp, mq, a);
+  return cudaGetLastError();
+}
+
 template <bool P_MN, bool Q_MN>
 cudaError_t launch_product(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
   const int64_t slices = (a.depth + kDepth - 1) / kDepth;
@@ -371,6 +725,8 @@ cudaError_t launch_product(const Operand& p, const Operand& q, ProductArgs a, cu
     while (split < 8 && tiles(BN) * split * 2 <= 148 && slices >= split * 2 * 4) split *= 2;
     return launch_tiles<P_MN, Q_MN, BN, false>(p, q, a, split, stream);
   };
+  const int64_t pair_tiles = (a.rows_p + kPairTile - 1) / kPairTile * ((a.rows_q + kPairTile - 1) / kPairTile);
+  if (a.depth > 0 && pair_tiles >= 74 && pair_tiles < (int64_t{1} << 30)) return launch_pairs<P_MN, Q_MN>(p, q, a, stream);
   if (tiles(256) >= 148) return go(std::integral_constant<int, 256>{});
   if (tiles(128) >= 148) return go(std::integral_constant<int, 128>{});
   return go(std::integral_constant<int, 64>{});

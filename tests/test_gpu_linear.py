@@ -235,3 +235,45 @@ def test_linear_on_a_side_stream_and_in_a_graph(sizes):
         other = step()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(other, held))
+
+
+@pytest.mark.parametrize("sizes", [(257, 264, 128), (2300, 2304, 200), (2200, 2056, 72), (6000, 1001, 136)], ids=str)
+def test_large_products_match_oracle(sizes):
+    """Enough 256 x 256 tiles for every pair of SMs to take more than one, with ends inside tiles in each
+    direction."""
+    m, n, k = sizes
+    rng = np.random.default_rng(m)
+    x, w, r = matrix(rng, m, k, "bf16"), matrix(rng, n, k, "bf16", scale=k ** -0.5), matrix(rng, m, n, "bf16")
+    b = matrix(rng, 1, n, "bf16")[0]
+    y = opr.opr_linear(x, w, b, "silu", r)
+    X, W = to64(x), to64(w)
+    ry, rz = lo.linear(X, W, to64(b), "silu", to64(r))
+    bz = sum_bound(X, W, k) + (np.abs(rz) + 2) * 2.0 ** -23
+    within(y, ry, act_bound(rz, bz, "silu") + (np.abs(ry) + 4) * 2.0 ** -23, "bf16")
+    dy = matrix(rng, m, n, "bf16", scale=0.1)
+    dx, dw, _ = opr.opr_linear_bwd(dy, x, w)
+    within(dx, to64(dy) @ W, sum_bound(to64(dy), W.T, n), "bf16")
+    within(dw, to64(dy).T @ X, sum_bound(to64(dy).T, X.T, m), "bf16")
+    # the transposed problem has the same dw, transposed: other operands, other tiles
+    _, dwt, _ = opr.opr_linear_bwd(x, dy, torch.zeros(k, n, dtype=torch.bfloat16, device="cuda"), need_dx=False)
+    within(dwt, to64(x).T @ to64(dy), sum_bound(to64(x).T, to64(dy).T, m), "bf16")
+
+
+@pytest.mark.parametrize("sizes", [(3, 64, 4096), (300, 300, 4096), (6000, 1024, 512)], ids=str)
+def test_linear_reports_a_pipeline_timeout(sizes):
+    """With a wait limit of 0 every wait that is not already done gives up: the call reports it, the kernel
+    ends, and the next call with the usual limit is right.  (A wait may be done already: not every try trips.)"""
+    m, n, k = sizes
+    rng = np.random.default_rng(1)
+    x, w = matrix(rng, m, k, "bf16"), matrix(rng, n, k, "bf16")
+    want = opr.opr_linear(x, w)
+    torch.cuda.synchronize()
+    lib, st = opr.load_library(), status()
+    prev = lib.opr_testing_set_wait_limit_ns(0)
+    try:
+        opr.opr_linear(x, w, dev_status=st)
+        torch.cuda.synchronize()
+    finally:
+        lib.opr_testing_set_wait_limit_ns(prev)
+    assert opr.read_status(st) == [_abi.DEV_BITS[8]]
+    assert torch.equal(opr.opr_linear(x, w, dev_status=st.zero_()), want) and opr.read_status(st) == []
