@@ -177,7 +177,8 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle itself: building a Stream object costs as much as a small kernel
+    return torch._C._cuda_getCurrentRawStream(device.index if device.index is not None else torch.cuda.current_device())
 
 
 def _need_cuda(*ts: torch.Tensor) -> None:
@@ -639,24 +640,40 @@ def opr_rotary_frequencies(rot_dim: int, base: float, rule: str = "plain", facto
 def _heads(name: str, t: torch.Tensor, total: int | None = None, d: int | None = None,
            heads: int | None = None) -> int:
     """Checks rows of heads [total, heads, head_dim] (the heads of a token contiguous); their stride."""
-    if t.dim() != 3 or t.dtype not in _DT:
+    if t.dtype not in _DT or t.dim() != 3:
         raise OprError(f"{name} must be bf16, fp16 or fp32 [tokens, heads, head_dim]")
     if not t.is_cuda:
         raise OprError("tensors must live on a CUDA device")
-    for want, got in ((total, t.shape[0]), (heads, t.shape[1]), (d, t.shape[2])):
-        if want is not None and want != got:
-            raise OprError(f"{name} has shape {tuple(t.shape)}, which does not fit the other tensors")
-    width = t.shape[1] * t.shape[2]
-    if t.numel() == 0 or t.shape[0] == 1 and t[0].is_contiguous():
-        return width
-    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]) or t.stride(0) < width:
+    n, h, e = t.shape
+    if (total is not None and n != total) or (heads is not None and h != heads) or (d is not None and e != d):
+        raise OprError(f"{name} has shape {tuple(t.shape)}, which does not fit the other tensors")
+    if t.is_contiguous():
+        return h * e
+    st, sh, se = t.stride()
+    if n == 1 and (h == 1 or sh == e) and (e == 1 or se == 1):
+        return h * e
+    if (e > 1 and se != 1) or (h > 1 and sh != e) or st < h * e:
         raise OprError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0)
+    return st
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """Runs an entry point on the device's current stream, with the device current, and checks its status."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device))
+    if st != OPR_OK:
+        _check(st, name)
 
 
 def _one_device(call: str, first: torch.Tensor, *ts: torch.Tensor | None) -> None:
-    if any(t is not None and t.device != first.device for t in ts):
-        raise OprError(f"{call}: every tensor must be on one device")
+    device = first.device
+    for t in ts:
+        if t is not None and t.device != device:
+            raise OprError(f"{call}: every tensor must be on one device")
 
 
 def _rotation(call: str, x: torch.Tensor, pos_id, freq, row_map, dev_status) -> None:
@@ -690,12 +707,8 @@ def opr_rotary(x: torch.Tensor, pos_id: torch.Tensor, freq: torch.Tensor, interl
     _rotation("opr_rotary", x, pos_id, freq, row_map, dev_status)
     _one_device("opr_rotary", x, out)
     total, heads, d = x.shape
-    with torch.cuda.device(x.device):
-        st = load_library().opr_rotary(_ptr(x), _DT[x.dtype], xs, _ptr(out), _DT[out.dtype], ys, _ptr(pos_id),
-                                       _ptr(freq), 2 * freq.numel(), int(bool(interleaved)), float(scale),
-                                       int(bool(inverse)), _ptr(row_map), total, heads, d, _ptr(dev_status),
-                                       _stream(x.device))
-    _check(st, "opr_rotary")
+    _call("opr_rotary", x.device, _ptr(x), _DT[x.dtype], xs, _ptr(out), _DT[out.dtype], ys, _ptr(pos_id), _ptr(freq),
+          2 * freq.numel(), bool(interleaved), scale, bool(inverse), _ptr(row_map), total, heads, d, _ptr(dev_status))
     return out
 
 
@@ -740,13 +753,10 @@ def opr_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k
     if any(o.shape != t.shape or o.dtype not in _DT or o.dtype != out[0].dtype for o, t in zip(out, ins)):
         raise OprError("out must have the shapes of q, k and v and one type of bf16, fp16 or fp32")
     _one_device("opr_qk_norm_rope", q, k, v, q_weight, k_weight, *out)
-    with torch.cuda.device(q.device):
-        st = load_library().opr_qk_norm_rope(
-            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _DT[q.dtype], _ptr(q_weight), _ptr(k_weight), _DT[q_weight.dtype],
-            float(eps), _ptr(pos_id), _ptr(freq), 2 * freq.numel(), int(bool(interleaved)), float(scale),
-            _ptr(row_map), total, hq, k.shape[1], d, _ptr(out[0]), _ptr(out[1]), _ptr(out[2]) if v is not None else None,
-            _DT[out[0].dtype], _ptr(dev_status), _stream(q.device))
-    _check(st, "opr_qk_norm_rope")
+    _call("opr_qk_norm_rope", q.device, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _DT[q.dtype], _ptr(q_weight),
+          _ptr(k_weight), _DT[q_weight.dtype], eps, _ptr(pos_id), _ptr(freq), 2 * freq.numel(), bool(interleaved), scale,
+          _ptr(row_map), total, hq, k.shape[1], d, _ptr(out[0]), _ptr(out[1]), _ptr(out[2]) if v is not None else None,
+          _DT[out[0].dtype], _ptr(dev_status))
     return tuple(out)
 
 
@@ -792,15 +802,12 @@ def opr_qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k:
     _need_cuda(workspace)
     _one_device("opr_qk_norm_rope_bwd", q, workspace)
     dqw, dkw = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in range(2))
-    with torch.cuda.device(q.device):
-        st = load_library().opr_qk_norm_rope_bwd(
-            _ptr(dq), _ptr(dk), _ptr(dv), _DT[dq.dtype], _ptr(q), qs, _ptr(k), ks, _DT[q.dtype], _ptr(q_weight),
-            _ptr(k_weight), _DT[q_weight.dtype], float(eps), _ptr(pos_id), _ptr(freq), 2 * freq.numel(),
-            int(bool(interleaved)), float(scale), _ptr(row_map), total, hq, hkv, d, _ptr(out[0]), strides[0],
-            _ptr(out[1]), strides[1], _ptr(out[2]) if dv is not None else None, strides[2] if dv is not None else 0,
-            _DT[out[0].dtype], _ptr(dqw), _ptr(dkw), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _ptr(dev_status), _stream(q.device))
-    _check(st, "opr_qk_norm_rope_bwd")
+    _call("opr_qk_norm_rope_bwd", q.device, _ptr(dq), _ptr(dk), _ptr(dv), _DT[dq.dtype], _ptr(q), qs, _ptr(k), ks,
+          _DT[q.dtype], _ptr(q_weight), _ptr(k_weight), _DT[q_weight.dtype], eps, _ptr(pos_id), _ptr(freq),
+          2 * freq.numel(), bool(interleaved), scale, _ptr(row_map), total, hq, hkv, d, _ptr(out[0]), strides[0],
+          _ptr(out[1]), strides[1], _ptr(out[2]) if dv is not None else None, strides[2] if dv is not None else 0,
+          _DT[out[0].dtype], _ptr(dqw), _ptr(dkw), _ptr(workspace), workspace.numel() * workspace.element_size(),
+          _ptr(dev_status))
     return (*out, dqw, dkw)
 
 
@@ -811,13 +818,15 @@ def _matrix(name: str, t: torch.Tensor, dtypes=None, shape=None) -> int:
             str(x).replace("torch.", "") for x in (_DT if dtypes is None else dtypes)))
     if not t.is_cuda:
         raise OprError("tensors must live on a CUDA device")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise OprError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.numel() == 0 or (t.shape[0] == 1 and t[0].is_contiguous()):
-        return max(t.shape[1], 1)
-    if (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < t.shape[1]:
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise OprError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.is_contiguous():
+        return max(cols, 1)
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
         raise OprError(f"{name}: rows must be contiguous")
-    return t.stride(0)
+    return ld if rows > 1 else cols
 
 
 def _status_word(dev_status, device) -> torch.Tensor:
@@ -879,15 +888,12 @@ def opr_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
     z = torch.empty((m, n), dtype=x.dtype, device=x.device) if save_z else None
     _one_device("opr_linear", x, w, bias, residual, out)
     status = _status_word(dev_status, x.device)
-    lib = load_library()
-    need = int(lib.opr_linear_workspace_bytes(_ptr(x), ldx, _ptr(w), ldw, m, n, k))
+    need = load_library().opr_linear_workspace_bytes(_ptr(x), ldx, _ptr(w), ldw, m, n, k)
     workspace, ws_bytes = _scratch(workspace, need, x.device)
-    with torch.cuda.device(x.device):
-        st = lib.opr_linear(_ptr(x), ldx, _ptr(w), ldw, _DT[x.dtype], _ptr(bias), 0 if bias is None else _DT[bias.dtype],
-                            ACTIVATIONS[activation], _ptr(residual), ldr,
-                            0 if residual is None else _DT[residual.dtype], _ptr(out), ldy, _DT[out.dtype], _ptr(z), n,
-                            m, n, k, _ptr(workspace), ws_bytes, _ptr(status), _stream(x.device))
-    _check(st, "opr_linear")
+    _call("opr_linear", x.device, _ptr(x), ldx, _ptr(w), ldw, _DT[x.dtype], _ptr(bias),
+          0 if bias is None else _DT[bias.dtype], ACTIVATIONS[activation], _ptr(residual), ldr,
+          0 if residual is None else _DT[residual.dtype], _ptr(out), ldy, _DT[out.dtype], _ptr(z), n, m, n, k,
+          _ptr(workspace), ws_bytes, _ptr(status))
     return (out, z) if save_z else out
 
 
@@ -945,16 +951,11 @@ def opr_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.
     ldw_out = 0 if dw is None else _matrix("dw", dw, shape=(n, k))
     _one_device("opr_linear_bwd", x, w, dy, z, dx_residual, dx, dw)
     status = _status_word(dev_status, x.device)
-    lib = load_library()
-    need = int(lib.opr_linear_bwd_workspace_bytes(_ptr(dy), ldy, _ptr(x), ldx, _ptr(w), ldw, m, n, k,
-                                                  ACTIVATIONS[activation]))
+    need = load_library().opr_linear_bwd_workspace_bytes(_ptr(dy), ldy, _ptr(x), ldx, _ptr(w), ldw, m, n, k,
+                                                         ACTIVATIONS[activation])
     workspace, ws_bytes = _scratch(workspace, need, x.device)
-    with torch.cuda.device(x.device):
-        st = lib.opr_linear_bwd(_ptr(dy), ldy, _ptr(x), ldx, _ptr(w), ldw, _DT[x.dtype], _ptr(z), ldz,
-                                ACTIVATIONS[activation], _ptr(dx_residual), ldr,
-                                0 if dx_residual is None else _DT[dx_residual.dtype], _ptr(dx), ldx_out,
-                                0 if dx is None else _DT[dx.dtype], _ptr(dw), ldw_out,
-                                0 if dw is None else _DT[dw.dtype], _ptr(db), m, n, k, _ptr(workspace), ws_bytes,
-                                _ptr(status), _stream(x.device))
-    _check(st, "opr_linear_bwd")
+    _call("opr_linear_bwd", x.device, _ptr(dy), ldy, _ptr(x), ldx, _ptr(w), ldw, _DT[x.dtype], _ptr(z), ldz,
+          ACTIVATIONS[activation], _ptr(dx_residual), ldr, 0 if dx_residual is None else _DT[dx_residual.dtype], _ptr(dx),
+          ldx_out, 0 if dx is None else _DT[dx.dtype], _ptr(dw), ldw_out, 0 if dw is None else _DT[dw.dtype], _ptr(db),
+          m, n, k, _ptr(workspace), ws_bytes, _ptr(status))
     return dx, dw, db

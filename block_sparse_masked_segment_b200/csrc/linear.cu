@@ -4,6 +4,7 @@
 //   dz = dy act'(z);  db = sum over rows of dz;  dx = dz w;  dw = dz^T x
 // 16-bit operands, fp32 sums, each output rounded once.
 #include <algorithm>
+#include <atomic>
 
 #include "attn_common.cuh"
 #include "host_status.h"
@@ -141,10 +142,11 @@ __device__ __forceinline__ uint64_t depth_limit(uint64_t wait_ns, int slices) {
 constexpr int kProductThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
 constexpr int kProductSmem = 225 * 1024;
 
-template <int BN>
+template <bool Q_MN, int BN>
 struct TileSmem {
-  static constexpr int kStageBytes = kRowsP * 128 + (BN < 64 ? 64 : BN) * 128;
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int kRowsQ = Q_MN && BN < 64 ? 64 : BN;  // an MN-major chunk has 64 rows
+  static constexpr int kStageBytes = (kRowsP + kRowsQ) * 128;
+  static constexpr int kStages = 220 * 1024 / kStageBytes < 12 ? 220 * 1024 / kStageBytes : 12;
   alignas(1024) uint8_t ring[kStages][kStageBytes];
   uint64_t full[kStages], empty[kStages], done;
   uint32_t tmem_base;
@@ -160,7 +162,8 @@ template <bool P_MN, bool Q_MN, int BN, bool SWAP>
 __global__ void __launch_bounds__(kProductThreads, 1)
     product_tile_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ ProductArgs a) {
-  using Smem = TileSmem<BN>;
+  using Smem = TileSmem<Q_MN, BN>;
+  constexpr int kRowsQ = Smem::kRowsQ;
   constexpr int kStages = Smem::kStages;
   constexpr uint32_t kCols = BN < 32 ? 32 : BN;
   extern __shared__ uint8_t smem_raw[];
@@ -191,8 +194,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      constexpr int kRowsQ = Q_MN && BN < 64 ? 64 : BN;  // an MN-major chunk has 64 rows
-      constexpr uint32_t kBytes = (kRowsP + kRowsQ) * 128;
+      constexpr uint32_t kBytes = Smem::kStageBytes;
       int issued = 0;
       for (int j = 0; j < n; ++j) {
         const int s = j % kStages;
@@ -664,6 +666,20 @@ bool operand_map(CUtensorMap* map, const Operand& o, int64_t rows, int64_t depth
                       const_cast<void*>(o.p), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Lets a kernel use kProductSmem of shared memory, once per device and kernel.
+template <auto* kKernel>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (dev < 64 && (allowed.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+  if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <bool P_MN, bool Q_MN, int BN, bool SWAP>
 cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, int split, cudaStream_t stream) {
   CUtensorMap mp, mq;
@@ -672,11 +688,12 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, int 
   if (!operand_map(&mp, p, a.rows_p, depth, a.f16 != 0, kRowsP) ||
       !operand_map(&mq, q, a.rows_q, depth, a.f16 != 0, BN))
     return cudaErrorInvalidValue;
-  auto* kernel = product_tile_kernel<P_MN, Q_MN, BN, SWAP>;
-  static_assert(sizeof(TileSmem<BN>) + 1024 <= kProductSmem, "a tile's ring fits an SM");
-  static_assert((SWAP ? BN * kRowsP : kRowsP * (BN + 1)) * 4 <= static_cast<int>(sizeof(TileSmem<BN>::ring)),
+  constexpr auto* kernel = product_tile_kernel<P_MN, Q_MN, BN, SWAP>;
+  using Smem = TileSmem<Q_MN, BN>;
+  static_assert(sizeof(Smem) + 1024 <= kProductSmem, "a tile's ring fits an SM");
+  static_assert((SWAP ? BN * kRowsP : kRowsP * (BN + 1)) * 4 <= static_cast<int>(sizeof(Smem::ring)),
                 "the partial tile fits where the ring was");
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+  const cudaError_t e = allow_smem<kernel>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.tiles_p * split), static_cast<unsigned>(a.tiles_q));
@@ -702,8 +719,8 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cuda
   if (!operand_map(&mp, p, a.rows_p, a.depth, a.f16 != 0, kRowsP) ||
       !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, kRowsP))
     return cudaErrorInvalidValue;
-  auto* kernel = product_pair_kernel<P_MN, Q_MN>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+  constexpr auto* kernel = product_pair_kernel<P_MN, Q_MN>;
+  const cudaError_t e = allow_smem<kernel>();
   if (e != cudaSuccess) return e;
   a.tiles_p = static_cast<int32_t>((a.rows_p + kPairTile - 1) / kPairTile);
   a.tiles_q = (a.rows_q + kPairTile - 1) / kPairTile;
@@ -713,24 +730,39 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cuda
   return cudaGetLastError();
 }
 
-template <bool P_MN, bool Q_MN>
-cudaError_t launch_product(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
+// A launch of single tiles: the depth of each split over as many CTAs of a cluster
+// as fill the 148 SMs once, four slices or more to each.
+template <bool P_MN, bool Q_MN, int BN, bool SWAP>
+cudaError_t launch_split_tiles(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
+  a.tiles_p = static_cast<int32_t>((a.rows_p + kRowsP - 1) / kRowsP);
+  a.tiles_q = (a.rows_q + BN - 1) / BN;
+  const int64_t tiles = static_cast<int64_t>(a.tiles_p) * a.tiles_q;
   const int64_t slices = (a.depth + kDepth - 1) / kDepth;
-  auto tiles = [&](int bn) { return (a.rows_p + kRowsP - 1) / kRowsP * ((a.rows_q + bn - 1) / bn); };
-  auto go = [&](auto bn) {
-    constexpr int BN = decltype(bn)::value;
-    a.tiles_p = static_cast<int32_t>((a.rows_p + kRowsP - 1) / kRowsP);
-    a.tiles_q = (a.rows_q + BN - 1) / BN;
-    int split = 1;
-    while (split < 8 && tiles(BN) * split * 2 <= 148 && slices >= split * 2 * 4) split *= 2;
-    return launch_tiles<P_MN, Q_MN, BN, false>(p, q, a, split, stream);
-  };
-  const int64_t pair_tiles = (a.rows_p + kPairTile - 1) / kPairTile * ((a.rows_q + kPairTile - 1) / kPairTile);
-  if (a.depth > 0 && pair_tiles >= 74 && pair_tiles < (int64_t{1} << 30)) return launch_pairs<P_MN, Q_MN>(p, q, a, stream);
-  if (tiles(256) >= 148) return go(std::integral_constant<int, 256>{});
-  if (tiles(128) >= 148) return go(std::integral_constant<int, 128>{});
-  return go(std::integral_constant<int, 64>{});
+  const int64_t split = std::max<int64_t>(1, std::min<int64_t>({8, 148 / tiles, slices / 4}));
+  return launch_tiles<P_MN, Q_MN, BN, SWAP>(p, q, a, static_cast<int>(split), stream);
 }
+
+template <bool P_MN, bool Q_MN>
+cudaError_t launch_product(const Operand& p, const Operand& q, const ProductArgs& a, cudaStream_t stream) {
+  auto tiles = [&](int bn) { return (a.rows_p + kRowsP - 1) / kRowsP * ((a.rows_q + bn - 1) / bn); };
+  const int64_t pair_tiles =
+      (a.rows_p + kPairTile - 1) / kPairTile * ((a.rows_q + kPairTile - 1) / kPairTile);
+  if (a.depth > 0 && pair_tiles >= 74 && pair_tiles < (int64_t{1} << 30)) return launch_pairs<P_MN, Q_MN>(p, q, a, stream);
+  if (tiles(256) >= 148) return launch_split_tiles<P_MN, Q_MN, 256, false>(p, q, a, stream);
+  if (tiles(128) >= 148) return launch_split_tiles<P_MN, Q_MN, 128, false>(p, q, a, stream);
+  return launch_split_tiles<P_MN, Q_MN, 64, false>(p, q, a, stream);
+}
+
+// Few rows of x: the weight fills the tiles' 128 rows, the rows of x their columns.
+template <bool W_MN>
+cudaError_t launch_few_rows(const Operand& x, const Operand& w, ProductArgs a, cudaStream_t stream) {
+  const int64_t m = a.rows_p;
+  a.rows_p = a.rows_q;
+  a.rows_q = static_cast<int32_t>(m);
+  if (m <= 16) return launch_split_tiles<W_MN, false, 16, true>(w, x, a, stream);
+  return launch_split_tiles<W_MN, false, 64, true>(w, x, a, stream);
+}
+constexpr int64_t kFewRows = 64;
 
 }  // namespace
 
@@ -746,9 +778,9 @@ cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t m, int32_t
   args.dev_status = dev_status;
   args.wait_ns = wait_limit_ns();
   const bool a_mn = a.col != 1, b_mn = b.col != 1;
-  if (!a_mn && !b_mn) return launch_product<false, false>(a, b, args, stream);
-  if (!a_mn) return launch_product<false, true>(a, b, args, stream);
-  return launch_product<true, true>(a, b, args, stream);
+  if (a_mn) return launch_product<true, true>(a, b, args, stream);
+  if (m <= kFewRows) return b_mn ? launch_few_rows<true>(a, b, args, stream) : launch_few_rows<false>(a, b, args, stream);
+  return b_mn ? launch_product<false, true>(a, b, args, stream) : launch_product<false, false>(a, b, args, stream);
 }
 
 cudaError_t launch_pack(const Operand& from, int64_t rows, int64_t cols, void* to, int64_t ld, cudaStream_t stream) {
