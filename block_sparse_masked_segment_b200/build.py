@@ -18,6 +18,7 @@ import argparse
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -58,17 +59,21 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     if not force and not _stale(lib):
         return lib
     os.makedirs(LIB_DIR, exist_ok=True)
-    objs = []
     extra = ["-DOPR_DEBUG_CHECKS"] if debug else []
-    for src in SOURCES:
+
+    def compile_one(src: str):
         obj = os.path.join(LIB_DIR, src.replace(".cu", "_debug.o" if debug else ".o"))
         cmd = [NVCC, *nvcc_flags(verbose), *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0 or verbose:
-            sys.stderr.write(r.stdout + r.stderr)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}")
-        objs.append(obj)
+        return obj, subprocess.run(cmd, capture_output=True, text=True)
+
+    objs = []
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as pool:
+        for src, (obj, r) in zip(SOURCES, pool.map(compile_one, SOURCES)):
+            if r.returncode != 0 or verbose:
+                sys.stderr.write(r.stdout + r.stderr)
+            if r.returncode != 0:
+                raise RuntimeError(f"nvcc failed on {src}")
+            objs.append(obj)
     tmp = lib + ".tmp"
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)

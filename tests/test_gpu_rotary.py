@@ -33,7 +33,8 @@ def rotary_bound(x, rot, interleaved, scale):
 
 # total, heads, d, rot: one token, odd counts, pairs off the grid of eight, whole and part of the head
 SHAPES = [(1, 1, 64, 64), (1, 32, 128, 128), (3, 2, 128, 64), (37, 5, 80, 20), (129, 3, 256, 256), (65, 1, 96, 48),
-          (17, 7, 6, 2), (260, 8, 128, 32), (33, 2, 72, 64), (40, 2, 200, 16)]
+          (17, 7, 6, 2), (260, 8, 128, 32), (33, 2, 72, 64), (40, 2, 200, 16),
+          (700, 3, 80, 80), (450, 1, 48, 16), (300, 40, 128, 128)]
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
@@ -177,7 +178,8 @@ def weights(rng, d, dtype):
 
 
 QK_SHAPES = [(1, 1, 1, 64, 64), (1, 32, 8, 128, 128), (5, 3, 1, 128, 64), (67, 8, 2, 64, 32), (130, 4, 4, 256, 256),
-             (19, 2, 1, 80, 20), (300, 5, 1, 128, 128), (12, 2, 2, 6, 4), (21, 3, 3, 72, 64), (40, 1, 1, 200, 16)]
+             (19, 2, 1, 80, 20), (300, 5, 1, 128, 128), (12, 2, 2, 6, 4), (21, 3, 3, 72, 64), (40, 1, 1, 200, 16),
+             (700, 2, 1, 80, 80), (450, 1, 1, 48, 16), (310, 20, 2, 128, 96), (900, 1, 5, 256, 64)]
 
 
 @pytest.mark.parametrize("packed", [False, True])
