@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "layer.cuh"
+#include "sm100.cuh"
 
 namespace opr {
 namespace {
@@ -195,7 +196,9 @@ __global__ void __launch_bounds__(1024) head_grad_sum_kernel(const HeadArgs a, i
 //   half layout, rotated   entries 8c .. 8c+7 and pairs + 8c .. pairs + 8c + 7
 //   otherwise              entries 16c .. 16c + 15
 // so that a unit holds both entries of its eight pairs (pairs 8c .. 8c + 7) in either
-// layout, and a head is a group of kGroup lanes whose sums are a few shuffles.
+// layout, and a head is a group of G lanes whose sums are a few shuffles.  Entries
+// 2i, 2i + 1 of a unit are one packed fp32 pair: the arithmetic runs two entries an
+// instruction, which is what bounds these kernels next to HBM.
 constexpr int kThreadsVec = 256;
 
 template <typename T>
@@ -219,22 +222,39 @@ __device__ __forceinline__ Raw<T> load_unit(const T* p, int o1, int o2) {
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack(const Raw<T>& r, float (&f)[16]) {
-  const T* e = reinterpret_cast<const T*>(r.v);
+__device__ __forceinline__ void unpack(const Raw<T>& r, uint64_t (&f)[8]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) f[k] = as_float(e[k]);
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (std::is_same_v<T, float>) {
+      f[i] = f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    } else {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[i] = f2(v.x, v.y);
+    }
+  }
 }
 
-// Stores a unit; true when an fp16 entry is beyond the range.
+// Stores a unit.  For fp16, `top` follows the largest size written (NaN stays).
 template <typename T>
-__device__ __forceinline__ bool store_unit(T* p, int o1, int o2, const float (&f)[16]) {
+__device__ __forceinline__ void store_unit(T* p, int o1, int o2, const uint64_t (&f)[8], __half2& top) {
   Raw<T> r;
-  T* e = reinterpret_cast<T*>(r.v);
-  bool bad = false;
+  uint32_t* w = reinterpret_cast<uint32_t*>(r.v);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    bad |= beyond<T>(f[k]);
-    e[k] = from_float<T>(f[k]);
+  for (int i = 0; i < 8; ++i) {
+    float lo, hi;
+    f2_split(f[i], lo, hi);
+    if constexpr (std::is_same_v<T, float>) {
+      w[2 * i] = __float_as_uint(lo);
+      w[2 * i + 1] = __float_as_uint(hi);
+    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      w[i] = pack_bf16x2(lo, hi);
+    } else {
+      w[i] = pack_f16x2(lo, hi);
+      top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+    }
   }
   if constexpr (sizeof(T) == 4) {
     reinterpret_cast<uint4*>(p + o1)[0] = r.v[0];
@@ -245,55 +265,66 @@ __device__ __forceinline__ bool store_unit(T* p, int o1, int o2, const float (&f
     *reinterpret_cast<uint4*>(p + o1) = r.v[0];
     *reinterpret_cast<uint4*>(p + o2) = r.v[1];
   }
-  return bad;
+}
+__device__ __forceinline__ bool overflowed(__half2 top) {
+  const float2 t = __half22float2(top);
+  return !(t.x <= 65504.f) || !(t.y <= 65504.f);
 }
 
-// Rotates the unit's pairs by t = (cos, sin) of each, sin with the sign `sign`.
+// Rotates the unit's pairs.  t: for pairs 2i, 2i + 1, t[2i] = (cos, cos), t[2i + 1] = (sin, sin).
 template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate_unit(float (&x)[16], const float (&t)[16], float sign) {
+__device__ __forceinline__ void rotate_unit(uint64_t (&x)[8], const uint64_t (&t)[8]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int ia = INTERLEAVED ? 2 * k : k, ib = INTERLEAVED ? 2 * k + 1 : k + 8;
-    const float c = t[2 * k], s = sign * t[2 * k + 1];
-    const float va = x[ia], vb = x[ib];
-    x[ia] = va * c - vb * s;
-    x[ib] = vb * c + va * s;
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t c = t[2 * i], s = t[2 * i + 1];
+    float s0, s1;
+    f2_split(s, s0, s1);
+    if constexpr (INTERLEAVED) {
+      float c0, c1, a0, b0, a1, b1;
+      f2_split(c, c0, c1);
+      f2_split(x[2 * i], a0, b0);
+      f2_split(x[2 * i + 1], a1, b1);
+      x[2 * i] = ffma2(x[2 * i], f2(c0, c0), fmul2(f2(b0, a0), f2(-s0, s0)));
+      x[2 * i + 1] = ffma2(x[2 * i + 1], f2(c1, c1), fmul2(f2(b1, a1), f2(-s1, s1)));
+    } else {
+      const uint64_t a = x[i], b = x[4 + i];
+      x[i] = ffma2(a, c, fmul2(b, f2(-s0, -s1)));
+      x[4 + i] = ffma2(b, c, fmul2(a, s));
+    }
   }
 }
 
-// Tables in shared memory, as float4 [4][units] per token (cos, sin of two pairs) or
-// per weight (four entries): neighbouring lanes read neighbouring 16 bytes.
-__device__ __forceinline__ void read16(const float4* t, int units, int c, float (&f)[16]) {
+// A unit's 16 words of a table float4 [4][units]: neighbouring lanes read
+// neighbouring 16 bytes.
+__device__ __forceinline__ void read16(const float4* t, int units, int c, uint64_t (&f)[8]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const float4 x = t[q * units + c];
-    f[4 * q] = x.x;
-    f[4 * q + 1] = x.y;
-    f[4 * q + 2] = x.z;
-    f[4 * q + 3] = x.w;
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(t + q * units + c);
+    f[2 * q] = x.x;
+    f[2 * q + 1] = x.y;
   }
 }
 
-// cos and sin of `ntok` tokens from tok0 into cs [ntok][4][rot_units].
-__device__ __forceinline__ void fill_turns(const HeadArgs& a, int64_t tok0, int ntok, float4* cs) {
+// cos and sin of `ntok` tokens from tok0 into cs [ntok][4][pairs / 8], in the order
+// of rotate_unit; the transpose's have the sine negated.
+__device__ __forceinline__ void fill_turns(const HeadArgs& a, int64_t tok0, int ntok, bool transpose, float4* cs) {
   const int units = a.pairs / 8;
   for (int i = threadIdx.x; i < ntok * a.pairs; i += blockDim.x) {
     const int t = i / a.pairs, j = i % a.pairs;
     float c, s;
     turn(a.pos[tok0 + t], a.freq[j], a.scale, c, s);
-    const int unit = j / 8, k = j % 8;
-    reinterpret_cast<float2*>(cs + (t * 4 + k / 2) * units + unit)[k & 1] = make_float2(c, s);
+    float* to = reinterpret_cast<float*>(cs + (t * 4 + (j % 8) / 2) * units + j / 8) + (j & 1);
+    to[0] = c;
+    to[2] = transpose ? -s : s;
   }
 }
 
-// Weight w [d] into t [4][units]: entries in unit order.
-__device__ __forceinline__ void fill_weight(const HeadArgs& a, const void* w, float4* t) {
-  const int units = a.d / 16;
-  for (int i = threadIdx.x; i < a.d; i += blockDim.x) {
-    const int c = i / 16, k = i % 16;
-    const bool split = !a.interleaved && c < a.pairs / 8;
-    const int e = split ? (k < 8 ? 8 * c + k : a.pairs + 8 * c + k - 8) : 16 * c + k;
-    reinterpret_cast<float*>(t + (k / 4) * units + c)[k & 3] = load_typed(w, a.w_dtype, e);
+// The unit's entries of a weight.
+__device__ __forceinline__ void load_weight(const HeadArgs& a, const void* w, int o1, int o2, uint64_t (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = (i < 4 ? o1 : o2 - 8) + 2 * i;
+    f[i] = f2(load_typed(w, a.w_dtype, e), load_typed(w, a.w_dtype, e + 1));
   }
 }
 
@@ -304,95 +335,107 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return lo + hi;
+}
+
+// i / heads for i < tokens * heads, by a product: exact while i * heads < 2^32, which
+// the callers' choice of the tokens keeps (else the plain quotient).
+struct Quotient {
+  uint32_t heads, magic;
+};
+__device__ __forceinline__ int quotient(int i, const Quotient& q) {
+  return q.magic != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), q.magic)) : i / static_cast<int>(q.heads);
+}
+struct Quotients {
+  Quotient set[3];
+};
+
 // A block takes `tokens` tokens, forms their cos and sin once, and its groups of G
-// lanes walk the (token, head) items of all sets.
+// lanes walk each set's (token, head) items in rounds, the next round's loads in
+// flight.
 template <typename TI, typename TO, int G>
-__global__ void __launch_bounds__(kThreadsVec) heads_vec_kernel(const HeadArgs a, int32_t heads_total, int32_t tokens) {
+__global__ void __launch_bounds__(kThreadsVec) heads_vec_kernel(const HeadArgs a, const Quotients quot, int32_t tokens) {
+  constexpr int kGroups = kThreadsVec / G;
   extern __shared__ float4 tables[];
   const int units = a.d / 16, rot_units = a.pairs / 8;
-  float4* wt = tables;                                 // [2][4][units], with a norm
-  const bool norm = a.set[0].mode == kHeadNormRotate;  // of set 0 (and 1)
-  float4* cs = tables + (norm ? 8 * units : 0);        // [tokens][4][rot_units]
+  float4* cs = tables;                                                           // [tokens][4][rot_units]
+  int32_t* orow = reinterpret_cast<int32_t*>(tables + tokens * 4 * rot_units);  // [tokens], -1: not written
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * tokens;
   const int ntok = static_cast<int>(a.total - tok0 < tokens ? a.total - tok0 : tokens);
-  const int c = threadIdx.x % G;
-  const int items = ntok * heads_total;
-  const bool live = c < units;
-  const bool turns = c < rot_units;
+  const int c = threadIdx.x % G, group = threadIdx.x / G;
+  const bool live = c < units, turns = c < rot_units;
   const bool apart = !a.interleaved && turns;
   const int o1 = apart ? 8 * c : 16 * c, o2 = apart ? a.pairs + 8 * c : 16 * c + 8;
-  const float sign = a.inverse ? -1.f : 1.f;
+  const float inv_d = 1.f / a.d;
 
-  struct Item {
-    int t, h, si;
-  };
-  auto item_of = [&](int i) {
-    Item it;
-    it.t = i / heads_total;
-    it.h = i % heads_total;
-    it.si = 0;
-    while (it.h >= a.set[it.si].heads) it.h -= a.set[it.si++].heads;
-    return it;
-  };
-  auto fetch = [&](const Item& it) {
-    const HeadSet& s = a.set[it.si];
-    return load_unit(static_cast<const TI*>(s.x) + (tok0 + it.t) * s.x_stride + static_cast<int64_t>(it.h) * a.d, o1, o2);
-  };
-  int i = threadIdx.x / G;
-  Item it{};
+  int si = 0, base = 0;  // the round's set and its first item (both uniform in the block)
   Raw<TI> raw{};
-  if (i < items) {
-    it = item_of(i);
-    if (live) raw = fetch(it);  // in flight while the tables are made
+  int t = 0, h = 0;
+  bool valid = false;
+  auto fetch = [&]() {
+    const HeadSet& s = a.set[si];
+    const int i = base + group;
+    t = quotient(i, quot.set[si]);
+    h = i - t * s.heads;
+    valid = live && t < ntok;
+    if (valid)
+      raw = load_unit(static_cast<const TI*>(s.x) + (tok0 + t) * s.x_stride + static_cast<int64_t>(h) * a.d, o1, o2);
+  };
+  fetch();  // in flight while the tables are made
+  fill_turns(a, tok0, ntok, a.inverse != 0, cs);
+  bool lost = false;
+  for (int i = threadIdx.x; i < ntok; i += kThreadsVec) {
+    const int64_t r = a.row_map != nullptr ? a.row_map[tok0 + i] : tok0 + i;
+    const bool in = r >= 0 && r < a.total;
+    lost |= !in;
+    orow[i] = in ? static_cast<int32_t>(r) : -1;
   }
-  fill_turns(a, tok0, ntok, cs);
-  if (norm)
-    for (int s = 0; s < 2; ++s) fill_weight(a, a.set[s].w, wt + 4 * s * units);
   __syncthreads();
-  bool bad = false, lost = false;
-  // all lanes of a warp stay in the loop for the shuffles
-  for (int first = threadIdx.x / 32 * (32 / G); first < items; first += kThreadsVec / G, i += kThreadsVec / G) {
-    const Item now = it;
-    float x[16];
+  __half2 top = __float2half2_rn(0.f);
+  uint64_t w[8];
+  if (a.set[0].mode == kHeadNormRotate) load_weight(a, a.set[0].w, live ? o1 : 0, live ? o2 : 8, w);
+  while (true) {
+    const HeadSet& s = a.set[si];
+    uint64_t x[8];
     unpack(raw, x);
-    const bool valid = i < items && live;
-    if (i + kThreadsVec / G < items) {
-      it = item_of(i + kThreadsVec / G);
-      if (live) raw = fetch(it);
+    const int now_t = t, now_h = h, now_si = si;
+    const bool now_valid = valid;
+    base += kGroups;
+    if (base >= ntok * s.heads) {
+      base = 0;
+      ++si;
     }
-    const HeadSet& s = a.set[now.si];
-    if (norm) {
-      float sum = 0.f;
+    const bool more = si < a.n_sets;
+    if (more) fetch();
+    if (s.mode == kHeadNormRotate) {
+      uint64_t sq = 0;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) sum = fmaf(x[k], x[k], sum);
-      sum = group_sum<G>(valid ? sum : 0.f);
-      if (valid && s.mode == kHeadNormRotate) {
-        const float rs = 1.f / sqrtf(sum / a.d + a.eps);
-        float w[16];
-        read16(wt + 4 * now.si * units, units, c, w);
+      for (int i = 0; i < 8; ++i) sq = ffma2(x[i], x[i], sq);
+      const float rs = rsqrtf(fmaf(group_sum<G>(now_valid ? sum2(sq) : 0.f), inv_d, a.eps));
+      const uint64_t rs2 = f2(rs, rs);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] *= rs * w[k];
+      for (int i = 0; i < 8; ++i) x[i] = fmul2(fmul2(x[i], rs2), w[i]);
+    }
+    const int to = now_valid ? orow[now_t] : -1;
+    if (to >= 0) {
+      if (turns && s.mode != kHeadCopy) {
+        uint64_t cw[8];
+        read16(cs + now_t * 4 * rot_units, rot_units, c, cw);
+        if (a.interleaved)
+          rotate_unit<true>(x, cw);
+        else
+          rotate_unit<false>(x, cw);
       }
+      store_unit(static_cast<TO*>(s.y) + to * s.y_stride + static_cast<int64_t>(now_h) * a.d, o1, o2, x, top);
     }
-    if (!valid) continue;
-    const int64_t tok = tok0 + now.t;
-    const int64_t orow = a.row_map != nullptr ? a.row_map[tok] : tok;
-    if (orow < 0 || orow >= a.total) {
-      lost = true;
-      continue;
-    }
-    if (turns && s.mode != kHeadCopy) {
-      float t[16];
-      read16(cs + now.t * 4 * rot_units, rot_units, c, t);
-      if (a.interleaved)
-        rotate_unit<true>(x, t, sign);
-      else
-        rotate_unit<false>(x, t, sign);
-    }
-    bad |= store_unit(static_cast<TO*>(s.y) + orow * s.y_stride + static_cast<int64_t>(now.h) * a.d, o1, o2, x);
+    if (!more) break;
+    if (si != now_si && a.set[si].mode == kHeadNormRotate) load_weight(a, a.set[si].w, live ? o1 : 0, live ? o2 : 8, w);
   }
   if (a.dev_status != nullptr) {
-    if (bad) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
+    if (overflowed(top)) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
     if (lost) atomicOr(a.dev_status, OPR_DEV_BAD_INPUT);
   }
 }
@@ -401,33 +444,37 @@ __global__ void __launch_bounds__(kThreadsVec) heads_vec_kernel(const HeadArgs a
 // heads; a block walks its set's tiles of `tokens` tokens with its groups, and keeps
 // its sums for w in registers, entry by entry of the lanes' units.
 struct GradBlocks {
-  int32_t first[4];  // blocks of set i: first[i] .. first[i + 1] - 1
+  int32_t first[4];   // blocks of set i: first[i] .. first[i + 1] - 1
+  int32_t tokens[3];  // of a tile of set i
+  int32_t cs_bytes;   // of the largest tile's table
 };
 
 template <typename TI, typename TG, typename TO, int G>
 __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const HeadArgs a, const GradBlocks deal,
-                                                                        int32_t max_tokens) {
+                                                                        const Quotients quot) {
   extern __shared__ float4 tables[];
   constexpr int kGroups = kThreadsVec / G;
   int si = 0;
   while (static_cast<int>(blockIdx.x) >= deal.first[si + 1]) ++si;
   const HeadSet& s = a.set[si];
+  const bool copy = s.mode == kHeadCopy;
   const int units = a.d / 16, rot_units = a.pairs / 8;
-  float4* wt = tables;                                                  // [4][units]
-  float* red = reinterpret_cast<float*>(tables + 4 * units);            // [groups][d]
-  float4* cs = tables + 4 * units + kGroups * 4 * units;                // [tokens][4][rot_units]
+  float4* cs = tables;                                                                             // [tokens][4][rot_units]
+  float* red = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(tables) + deal.cs_bytes);  // [groups][d]
   const int block = static_cast<int>(blockIdx.x) - deal.first[si], blocks = deal.first[si + 1] - deal.first[si];
-  // items a tile: about eight to a group
-  const int tokens = min(max_tokens, max(1, 8 * kGroups / s.heads));
+  const int tokens = deal.tokens[si];
   const int64_t tiles = (a.total + tokens - 1) / tokens;
-  const int c = threadIdx.x % G;
-  const bool live = c < units, turns = c < rot_units && s.mode != kHeadCopy;
+  const int c = threadIdx.x % G, group = threadIdx.x / G;
+  const bool live = c < units, turns = c < rot_units && !copy;
   const bool apart = !a.interleaved && c < rot_units;
   const int o1 = apart ? 8 * c : 16 * c, o2 = apart ? a.pairs + 8 * c : 16 * c + 8;
   const float inv_d = 1.f / a.d;
-  float acc[16] = {};
-  bool bad = false, lost = false;
-  if (s.mode != kHeadCopy) fill_weight(a, s.w, wt);
+  uint64_t acc[8], w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0;
+  if (!copy) load_weight(a, s.w, live ? o1 : 0, live ? o2 : 8, w);
+  __half2 top = __float2half2_rn(0.f);
+  bool lost = false;
 
   for (int64_t tile = block; tile < tiles; tile += blocks) {
     const int64_t tok0 = tile * tokens;
@@ -435,79 +482,80 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
     const int items = ntok * s.heads;
     Raw<TI> rx{};
     Raw<TG> rg{};
-    bool known = false;  // of the item held: its gradient row is in range
+    int t = 0, h = 0;
+    bool valid = false;
     auto fetch = [&](int i) {
-      const int t = i / s.heads, h = i % s.heads;
+      t = quotient(i, quot.set[si]);
+      h = i - t * s.heads;
+      valid = live && t < ntok;
+      if (!valid) return;
       const int64_t tok = tok0 + t;
-      const int64_t grow = a.row_map != nullptr ? a.row_map[tok] : tok;
-      known = grow >= 0 && grow < a.total;
-      if (!known) {
-        lost = true;
-        return;
+      int64_t grow = tok;
+      if (a.row_map != nullptr) {
+        grow = a.row_map[tok];
+        valid = grow >= 0 && grow < a.total;
+        lost |= !valid;
+        if (!valid) return;
       }
-      if (!live) return;
       rg = load_unit(static_cast<const TG*>(s.dy) + grow * s.dy_stride + static_cast<int64_t>(h) * a.d, o1, o2);
-      if (s.mode != kHeadCopy)
+      if (!copy)
         rx = load_unit(static_cast<const TI*>(s.x) + tok * s.x_stride + static_cast<int64_t>(h) * a.d, o1, o2);
     };
-    int i = threadIdx.x / G;
-    if (i < items) fetch(i);
-    __syncthreads();  // the tile before has been read
-    if (s.mode != kHeadCopy) fill_turns(a, tok0, ntok, cs);
-    __syncthreads();
-    for (int first = threadIdx.x / 32 * (32 / G); first < items; first += kGroups, i += kGroups) {
-      float x[16], g[16];
+    fetch(group);
+    if (!copy) {
+      __syncthreads();  // the tile before has been read
+      fill_turns(a, tok0, ntok, true, cs);
+      __syncthreads();
+    }
+    for (int base = 0; base < items; base += kGroups) {
+      uint64_t x[8], g[8];
       unpack(rx, x);
       unpack(rg, g);
-      const bool valid = i < items && live && known;
-      const int t = i / s.heads, h = i % s.heads;
-      if (i + kGroups < items) fetch(i + kGroups);
-      if (turns && valid) {
-        float w[16];
-        read16(cs + t * 4 * rot_units, rot_units, c, w);
+      const bool now_valid = valid;
+      const int now_t = t, now_h = h;
+      if (base + kGroups < items) fetch(base + kGroups + group);
+      if (turns && now_valid) {
+        uint64_t cw[8];
+        read16(cs + now_t * 4 * rot_units, rot_units, c, cw);
         if (a.interleaved)
-          rotate_unit<true>(g, w, -1.f);
+          rotate_unit<true>(g, cw);
         else
-          rotate_unit<false>(g, w, -1.f);
+          rotate_unit<false>(g, cw);
       }
-      if (s.mode != kHeadCopy) {
-        // sum of x^2 and of u x in one round of shuffles; xh = x rs comes after
-        float w[16], sq = 0.f, ux = 0.f;
-        read16(wt, units, live ? c : 0, w);
+      if (!copy) {
+        // sums of x^2 and of u x in one round of shuffles (u = g w); xh = x rs after it
+        uint64_t u[8], sq = 0, ux = 0;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          sq = fmaf(x[k], x[k], sq);
-          w[k] *= g[k];  // u
-          ux = fmaf(w[k], x[k], ux);
+        for (int i = 0; i < 8; ++i) {
+          u[i] = fmul2(g[i], w[i]);
+          sq = ffma2(x[i], x[i], sq);
+          ux = ffma2(u[i], x[i], ux);
         }
-        sq = group_sum<G>(valid ? sq : 0.f);
-        ux = group_sum<G>(valid ? ux : 0.f);
-        if (!valid) continue;
-        const float rs = 1.f / sqrtf(sq * inv_d + a.eps);
-        const float mean = ux * rs * inv_d;  // of u xh
+        const float rs = rsqrtf(fmaf(group_sum<G>(now_valid ? sum2(sq) : 0.f), inv_d, a.eps));
+        const float mean = group_sum<G>(now_valid ? sum2(ux) : 0.f) * rs * inv_d;  // of u xh
+        if (now_valid) {
+          const uint64_t rs2 = f2(rs, rs), nm2 = f2(-mean, -mean);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float xh = x[k] * rs;
-          acc[k] = fmaf(g[k], xh, acc[k]);
-          g[k] = rs * (w[k] - xh * mean);
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t xh = fmul2(x[i], rs2);
+            acc[i] = ffma2(g[i], xh, acc[i]);
+            g[i] = fmul2(rs2, ffma2(xh, nm2, u[i]));
+          }
         }
       }
-      if (!valid) continue;
-      bad |= store_unit(static_cast<TO*>(s.y) + (tok0 + t) * s.y_stride + static_cast<int64_t>(h) * a.d, o1, o2, g);
+      if (now_valid)
+        store_unit(static_cast<TO*>(s.y) + (tok0 + now_t) * s.y_stride + static_cast<int64_t>(now_h) * a.d, o1, o2, g, top);
     }
   }
   if (a.dev_status != nullptr) {
-    if (bad) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
+    if (overflowed(top)) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
     if (lost) atomicOr(a.dev_status, OPR_DEV_BAD_INPUT);
   }
-  if (s.mode == kHeadCopy) return;
-  float* mine = red + (threadIdx.x / G) * a.d;
+  if (copy) return;
+  float* mine = red + group * a.d;
   if (live) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      mine[o1 + k] = acc[k];
-      mine[o2 + k] = acc[8 + k];
-    }
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint64_t*>(mine + (i < 4 ? o1 : o2 - 8) + 2 * i) = acc[i];
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.d; e += kThreadsVec) {
@@ -546,19 +594,42 @@ cudaError_t with_group(int32_t d, F f) {
   return f(std::integral_constant<int, 16>{});
 }
 
-cudaError_t launch_heads_vec(const HeadArgs& a, int32_t heads, int32_t x_dtype, int32_t y_dtype, cudaStream_t stream) {
+// Quotients by the sets' heads for items of up to `tokens` tokens.
+Quotients quotients(const HeadArgs& a, const int32_t (&tokens)[3]) {
+  Quotients q{};
+  for (int i = 0; i < a.n_sets; ++i) {
+    const uint64_t heads = static_cast<uint64_t>(a.set[i].heads);
+    q.set[i].heads = static_cast<uint32_t>(heads);
+    // items of the last round may reach past the tokens by a round of groups
+    const uint64_t items = static_cast<uint64_t>(tokens[i]) * heads + 2 * kThreadsVec;
+    q.set[i].magic = heads > 1 && items * heads < (uint64_t{1} << 32)
+                         ? static_cast<uint32_t>(((uint64_t{1} << 32) + heads - 1) / heads)
+                         : 0;
+  }
+  return q;
+}
+
+cudaError_t launch_heads_vec(const HeadArgs& a, int32_t x_dtype, int32_t y_dtype, cudaStream_t stream) {
   return with_group(a.d, [&](auto g) {
     constexpr int G = decltype(g)::value;
-    // four items a group where the batch has them and the tables stay small, one
-    // token a block for small batches
-    const int64_t want = 4 * (kThreadsVec / G) / heads;
-    const int32_t tokens = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({want, 32, a.total / 148})));
-    const bool norm = a.set[0].mode == kHeadNormRotate;
-    const size_t smem = sizeof(float4) * (static_cast<size_t>(tokens) * 4 * (a.pairs / 8) + (norm ? 8 * (a.d / 16) : 0));
+    int32_t fewest = a.set[0].heads, heads = 0;
+    for (int i = 0; i < a.n_sets; ++i) {
+      fewest = std::min(fewest, a.set[i].heads);
+      heads += a.set[i].heads;
+    }
+    // full rounds for the smallest set and at least kRounds of them in all, where the
+    // batch has the tokens; small batches spread over the SMs instead
+    constexpr int kGroups = kThreadsVec / G, kRounds = 8;
+    const int64_t want = std::max<int64_t>((kGroups + fewest - 1) / fewest, (kRounds * kGroups + heads - 1) / heads);
+    const int32_t tokens =
+        static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({want, 32, a.total / (2 * 148)})));
+    const size_t smem = sizeof(float4) * tokens * 4 * (a.pairs / 8) + sizeof(int32_t) * tokens;
     const unsigned blocks = static_cast<unsigned>((a.total + tokens - 1) / tokens);
+    const int32_t each[3] = {tokens, tokens, tokens};
+    const Quotients q = quotients(a, each);
     return with_type(x_dtype, [&](auto ti) {
       return with_type(y_dtype, [&](auto to) {
-        heads_vec_kernel<decltype(ti), decltype(to), G><<<blocks, kThreadsVec, smem, stream>>>(a, heads, tokens);
+        heads_vec_kernel<decltype(ti), decltype(to), G><<<blocks, kThreadsVec, smem, stream>>>(a, q, tokens);
         return cudaGetLastError();
       });
     });
@@ -571,7 +642,7 @@ cudaError_t launch_heads(const HeadArgs& a, int32_t x_dtype, int32_t y_dtype, cu
   int32_t heads = 0;
   for (int i = 0; i < a.n_sets; ++i) heads += a.set[i].heads;
   if (a.total == 0 || heads == 0) return cudaSuccess;
-  if (vector_ready(a, x_dtype, y_dtype, y_dtype)) return launch_heads_vec(a, heads, x_dtype, y_dtype, stream);
+  if (vector_ready(a, x_dtype, y_dtype, y_dtype)) return launch_heads_vec(a, x_dtype, y_dtype, stream);
   const int64_t blocks = (a.total * heads + kWarps - 1) / kWarps;
   return with_type(x_dtype, [&](auto ti) {
     return with_type(y_dtype, [&](auto to) {
@@ -590,7 +661,6 @@ cudaError_t launch_head_grads_vec(const HeadArgs& a, int32_t x_dtype, int32_t dy
   // v counted whether it is there or not: the sums for w do not depend on it
   const int32_t heads = a.set[0].heads + 2 * a.set[1].heads;
   GradBlocks deal{};
-  const int32_t tokens = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(32, a.total / 148)));
   for (int i = 0; i < 3; ++i) {
     int64_t n = 0;
     if (i < a.n_sets) {
@@ -602,8 +672,16 @@ cudaError_t launch_head_grads_vec(const HeadArgs& a, int32_t x_dtype, int32_t dy
   }
   return with_group(a.d, [&](auto g) {
     constexpr int G = decltype(g)::value;
-    const int units = a.d / 16;
-    const size_t smem = sizeof(float4) * (4 * units + kThreadsVec / G * 4 * units + static_cast<size_t>(tokens) * 4 * (a.pairs / 8));
+    int32_t most = 1;
+    for (int i = 0; i < a.n_sets; ++i) {
+      // about eight rounds a tile, at least a tile a block
+      const int64_t want = (8 * (kThreadsVec / G) + a.set[i].heads - 1) / a.set[i].heads;
+      deal.tokens[i] = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({want, 32, a.total / blocks[i]})));
+      most = std::max(most, deal.tokens[i]);
+    }
+    deal.cs_bytes = static_cast<int32_t>(sizeof(float4)) * most * 4 * (a.pairs / 8);
+    const Quotients q = quotients(a, deal.tokens);
+    const size_t smem = deal.cs_bytes + sizeof(float) * (kThreadsVec / G) * a.d;
     return with_type(x_dtype, [&](auto ti) {
       return with_type(dy_dtype, [&](auto tg) {
         return with_type(dx_dtype, [&](auto to) {
@@ -616,7 +694,7 @@ cudaError_t launch_head_grads_vec(const HeadArgs& a, int32_t x_dtype, int32_t dy
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
             if (e != cudaSuccess) return e;
           }
-          kernel<<<deal.first[3], kThreadsVec, smem, stream>>>(a, deal, tokens);
+          kernel<<<deal.first[3], kThreadsVec, smem, stream>>>(a, deal, q);
           return cudaGetLastError();
         });
       });
