@@ -192,38 +192,59 @@ __global__ void __launch_bounds__(1024) head_grad_sum_kernel(const HeadArgs a, i
 
 // ---------------------------------------------------------------- vector form
 // For heads whose rows start on 16-byte boundaries, d a multiple of 16 and the pairs
-// a multiple of 8.  A head is d / 16 units of two 8-entry vectors, one unit a lane:
-//   half layout, rotated   entries 8c .. 8c+7 and pairs + 8c .. pairs + 8c + 7
-//   otherwise              entries 16c .. 16c + 15
-// so that a unit holds both entries of its eight pairs (pairs 8c .. 8c + 7) in either
-// layout, and a head is a group of G lanes whose sums are a few shuffles.  Entries
-// 2i, 2i + 1 of a unit are one packed fp32 pair: the arithmetic runs two entries an
-// instruction, which is what bounds these kernels next to HBM.
+// a multiple of 8.  A head is d / 16 units of 16 entries, one unit a lane, a head a
+// group of G lanes whose sums are a few shuffles.  A unit is 16 / VW vectors of VW
+// entries: eight where all types have 16 bits, four where one is fp32, so that
+// neighbouring lanes read neighbouring 16 bytes of the widest type (vectors side by
+// side in a lane instead, 32 or 64 bytes from lane to lane, took 1.1 to 1.4 times as
+// long).  Vector q of lane c lies at VW c + q (rotated entries) / (16 / VW) among the
+// rotated entries, alike among those behind: either layout's unit then holds both
+// entries of its eight pairs, and in the half layout the first eight entries are the
+// pairs' first ones.  Entries 2i, 2i + 1 of a unit are one packed fp32 pair: the
+// arithmetic runs two entries an instruction.
 constexpr int kThreadsVec = 256;
 
-template <typename T>
-struct Raw {  // a unit as loaded
-  uint4 v[sizeof(T) == 4 ? 4 : 2];
+template <int VW>
+struct UnitAt {
+  int first, step;  // of the vectors; entry of vector q: first + q * step
+  __device__ __forceinline__ UnitAt(const HeadArgs& a, int c) {
+    const int rot = 2 * a.pairs, rot_units = a.pairs / 8;
+    const bool r = c < rot_units;
+    first = r ? VW * c : rot + VW * (c - rot_units);
+    step = (r ? rot : a.d - rot) / (16 / VW);
+  }
+  __device__ __forceinline__ int operator[](int q) const { return first + q * step; }
 };
 
 template <typename T>
-__device__ __forceinline__ Raw<T> load_unit(const T* p, int o1, int o2) {
+struct Raw {  // a unit as loaded
+  uint32_t w[4 * sizeof(T)];
+};
+
+template <int VW, typename T>
+__device__ __forceinline__ Raw<T> load_unit(const T* p, const UnitAt<VW>& at) {
+  constexpr int kWords = VW * sizeof(T) / 4;  // of a vector: 2 or 4
   Raw<T> r;
-  if constexpr (sizeof(T) == 4) {
-    r.v[0] = reinterpret_cast<const uint4*>(p + o1)[0];
-    r.v[1] = reinterpret_cast<const uint4*>(p + o1)[1];
-    r.v[2] = reinterpret_cast<const uint4*>(p + o2)[0];
-    r.v[3] = reinterpret_cast<const uint4*>(p + o2)[1];
-  } else {
-    r.v[0] = *reinterpret_cast<const uint4*>(p + o1);
-    r.v[1] = *reinterpret_cast<const uint4*>(p + o2);
+#pragma unroll
+  for (int q = 0; q < 16 / VW; ++q) {
+    if constexpr (kWords == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p + at[q]);
+      r.w[2 * q] = v.x;
+      r.w[2 * q + 1] = v.y;
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + at[q]);
+      r.w[4 * q] = v.x;
+      r.w[4 * q + 1] = v.y;
+      r.w[4 * q + 2] = v.z;
+      r.w[4 * q + 3] = v.w;
+    }
   }
   return r;
 }
 
 template <typename T>
 __device__ __forceinline__ void unpack(const Raw<T>& r, uint64_t (&f)[8]) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
+  const auto& w = r.w;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (std::is_same_v<T, float>) {
@@ -238,32 +259,30 @@ __device__ __forceinline__ void unpack(const Raw<T>& r, uint64_t (&f)[8]) {
 }
 
 // Stores a unit.  For fp16, `top` follows the largest size written (NaN stays).
-template <typename T>
-__device__ __forceinline__ void store_unit(T* p, int o1, int o2, const uint64_t (&f)[8], __half2& top) {
+template <int VW, typename T>
+__device__ __forceinline__ void store_unit(T* p, const UnitAt<VW>& at, const uint64_t (&f)[8], __half2& top) {
+  constexpr int kWords = VW * sizeof(T) / 4;
   Raw<T> r;
-  uint32_t* w = reinterpret_cast<uint32_t*>(r.v);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float lo, hi;
     f2_split(f[i], lo, hi);
     if constexpr (std::is_same_v<T, float>) {
-      w[2 * i] = __float_as_uint(lo);
-      w[2 * i + 1] = __float_as_uint(hi);
+      r.w[2 * i] = __float_as_uint(lo);
+      r.w[2 * i + 1] = __float_as_uint(hi);
     } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-      w[i] = pack_bf16x2(lo, hi);
+      r.w[i] = pack_bf16x2(lo, hi);
     } else {
-      w[i] = pack_f16x2(lo, hi);
-      top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+      r.w[i] = pack_f16x2(lo, hi);
+      top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __half2*>(&r.w[i])));
     }
   }
-  if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<uint4*>(p + o1)[0] = r.v[0];
-    reinterpret_cast<uint4*>(p + o1)[1] = r.v[1];
-    reinterpret_cast<uint4*>(p + o2)[0] = r.v[2];
-    reinterpret_cast<uint4*>(p + o2)[1] = r.v[3];
-  } else {
-    *reinterpret_cast<uint4*>(p + o1) = r.v[0];
-    *reinterpret_cast<uint4*>(p + o2) = r.v[1];
+#pragma unroll
+  for (int q = 0; q < 16 / VW; ++q) {
+    if constexpr (kWords == 2)
+      *reinterpret_cast<uint2*>(p + at[q]) = make_uint2(r.w[2 * q], r.w[2 * q + 1]);
+    else
+      *reinterpret_cast<uint4*>(p + at[q]) = make_uint4(r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
   }
 }
 __device__ __forceinline__ bool overflowed(__half2 top) {
@@ -307,23 +326,28 @@ __device__ __forceinline__ void read16(const float4* t, int units, int c, uint64
 
 // cos and sin of `ntok` tokens from tok0 into cs [ntok][4][pairs / 8], in the order
 // of rotate_unit; the transpose's have the sine negated.
+template <int VW>
 __device__ __forceinline__ void fill_turns(const HeadArgs& a, int64_t tok0, int ntok, bool transpose, float4* cs) {
   const int units = a.pairs / 8;
+  const int per = a.interleaved ? VW / 2 : VW;  // pairs that a vector (of the first halves) begins
+  const int span = units * per;                 // pairs that one vector of each lane begins
   for (int i = threadIdx.x; i < ntok * a.pairs; i += blockDim.x) {
     const int t = i / a.pairs, j = i % a.pairs;
     float c, s;
     turn(a.pos[tok0 + t], a.freq[j], a.scale, c, s);
-    float* to = reinterpret_cast<float*>(cs + (t * 4 + (j % 8) / 2) * units + j / 8) + (j & 1);
+    const int unit = j % span / per, slot = j / span * per + j % per;
+    float* to = reinterpret_cast<float*>(cs + (t * 4 + slot / 2) * units + unit) + (slot & 1);
     to[0] = c;
     to[2] = transpose ? -s : s;
   }
 }
 
 // The unit's entries of a weight.
-__device__ __forceinline__ void load_weight(const HeadArgs& a, const void* w, int o1, int o2, uint64_t (&f)[8]) {
+template <int VW>
+__device__ __forceinline__ void load_weight(const HeadArgs& a, const void* w, const UnitAt<VW>& at, uint64_t (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int e = (i < 4 ? o1 : o2 - 8) + 2 * i;
+    const int e = at[2 * i / VW] + 2 * i % VW;
     f[i] = f2(load_typed(w, a.w_dtype, e), load_typed(w, a.w_dtype, e + 1));
   }
 }
@@ -356,8 +380,8 @@ struct Quotients {
 // A block takes `tokens` tokens, forms their cos and sin once, and its groups of G
 // lanes walk each set's (token, head) items in rounds, the next round's loads in
 // flight.
-template <typename TI, typename TO, int G>
-__global__ void __launch_bounds__(kThreadsVec) heads_vec_kernel(const HeadArgs a, const Quotients quot, int32_t tokens) {
+template <typename TI, typename TO, int VW, int G>
+__global__ void __launch_bounds__(kThreadsVec, 4) heads_vec_kernel(const HeadArgs a, const Quotients quot, int32_t tokens) {
   constexpr int kGroups = kThreadsVec / G;
   extern __shared__ float4 tables[];
   const int units = a.d / 16, rot_units = a.pairs / 8;
@@ -367,8 +391,7 @@ __global__ void __launch_bounds__(kThreadsVec) heads_vec_kernel(const HeadArgs a
   const int ntok = static_cast<int>(a.total - tok0 < tokens ? a.total - tok0 : tokens);
   const int c = threadIdx.x % G, group = threadIdx.x / G;
   const bool live = c < units, turns = c < rot_units;
-  const bool apart = !a.interleaved && turns;
-  const int o1 = apart ? 8 * c : 16 * c, o2 = apart ? a.pairs + 8 * c : 16 * c + 8;
+  const UnitAt<VW> at(a, live ? c : 0);
   const float inv_d = 1.f / a.d;
 
   int si = 0, base = 0;  // the round's set and its first item (both uniform in the block)
@@ -382,10 +405,10 @@ __global__ void __launch_bounds__(kThreadsVec) heads_vec_kernel(const HeadArgs a
     h = i - t * s.heads;
     valid = live && t < ntok;
     if (valid)
-      raw = load_unit(static_cast<const TI*>(s.x) + (tok0 + t) * s.x_stride + static_cast<int64_t>(h) * a.d, o1, o2);
+      raw = load_unit(static_cast<const TI*>(s.x) + (tok0 + t) * s.x_stride + static_cast<int64_t>(h) * a.d, at);
   };
   fetch();  // in flight while the tables are made
-  fill_turns(a, tok0, ntok, a.inverse != 0, cs);
+  fill_turns<VW>(a, tok0, ntok, a.inverse != 0, cs);
   bool lost = false;
   for (int i = threadIdx.x; i < ntok; i += kThreadsVec) {
     const int64_t r = a.row_map != nullptr ? a.row_map[tok0 + i] : tok0 + i;
@@ -396,7 +419,7 @@ __global__ void __launch_bounds__(kThreadsVec) heads_vec_kernel(const HeadArgs a
   __syncthreads();
   __half2 top = __float2half2_rn(0.f);
   uint64_t w[8];
-  if (a.set[0].mode == kHeadNormRotate) load_weight(a, a.set[0].w, live ? o1 : 0, live ? o2 : 8, w);
+  if (a.set[0].mode == kHeadNormRotate) load_weight(a, a.set[0].w, at, w);
   while (true) {
     const HeadSet& s = a.set[si];
     uint64_t x[8];
@@ -429,10 +452,10 @@ __global__ void __launch_bounds__(kThreadsVec) heads_vec_kernel(const HeadArgs a
         else
           rotate_unit<false>(x, cw);
       }
-      store_unit(static_cast<TO*>(s.y) + to * s.y_stride + static_cast<int64_t>(now_h) * a.d, o1, o2, x, top);
+      store_unit(static_cast<TO*>(s.y) + to * s.y_stride + static_cast<int64_t>(now_h) * a.d, at, x, top);
     }
     if (!more) break;
-    if (si != now_si && a.set[si].mode == kHeadNormRotate) load_weight(a, a.set[si].w, live ? o1 : 0, live ? o2 : 8, w);
+    if (si != now_si && a.set[si].mode == kHeadNormRotate) load_weight(a, a.set[si].w, at, w);
   }
   if (a.dev_status != nullptr) {
     if (overflowed(top)) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
@@ -449,7 +472,7 @@ struct GradBlocks {
   int32_t cs_bytes;   // of the largest tile's table
 };
 
-template <typename TI, typename TG, typename TO, int G>
+template <typename TI, typename TG, typename TO, int VW, int G>
 __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const HeadArgs a, const GradBlocks deal,
                                                                         const Quotients quot) {
   extern __shared__ float4 tables[];
@@ -466,13 +489,12 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
   const int64_t tiles = (a.total + tokens - 1) / tokens;
   const int c = threadIdx.x % G, group = threadIdx.x / G;
   const bool live = c < units, turns = c < rot_units && !copy;
-  const bool apart = !a.interleaved && c < rot_units;
-  const int o1 = apart ? 8 * c : 16 * c, o2 = apart ? a.pairs + 8 * c : 16 * c + 8;
+  const UnitAt<VW> at(a, live ? c : 0);
   const float inv_d = 1.f / a.d;
   uint64_t acc[8], w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0;
-  if (!copy) load_weight(a, s.w, live ? o1 : 0, live ? o2 : 8, w);
+  if (!copy) load_weight(a, s.w, at, w);
   __half2 top = __float2half2_rn(0.f);
   bool lost = false;
 
@@ -497,14 +519,14 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
         lost |= !valid;
         if (!valid) return;
       }
-      rg = load_unit(static_cast<const TG*>(s.dy) + grow * s.dy_stride + static_cast<int64_t>(h) * a.d, o1, o2);
+      rg = load_unit(static_cast<const TG*>(s.dy) + grow * s.dy_stride + static_cast<int64_t>(h) * a.d, at);
       if (!copy)
-        rx = load_unit(static_cast<const TI*>(s.x) + tok * s.x_stride + static_cast<int64_t>(h) * a.d, o1, o2);
+        rx = load_unit(static_cast<const TI*>(s.x) + tok * s.x_stride + static_cast<int64_t>(h) * a.d, at);
     };
     fetch(group);
     if (!copy) {
       __syncthreads();  // the tile before has been read
-      fill_turns(a, tok0, ntok, true, cs);
+      fill_turns<VW>(a, tok0, ntok, true, cs);
       __syncthreads();
     }
     for (int base = 0; base < items; base += kGroups) {
@@ -544,7 +566,7 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
         }
       }
       if (now_valid)
-        store_unit(static_cast<TO*>(s.y) + (tok0 + now_t) * s.y_stride + static_cast<int64_t>(now_h) * a.d, o1, o2, g, top);
+        store_unit(static_cast<TO*>(s.y) + (tok0 + now_t) * s.y_stride + static_cast<int64_t>(now_h) * a.d, at, g, top);
     }
   }
   if (a.dev_status != nullptr) {
@@ -555,7 +577,7 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
   float* mine = red + group * a.d;
   if (live) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint64_t*>(mine + (i < 4 ? o1 : o2 - 8) + 2 * i) = acc[i];
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint64_t*>(mine + at[2 * i / VW] + 2 * i % VW) = acc[i];
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.d; e += kThreadsVec) {
@@ -585,6 +607,10 @@ bool vector_ready(const HeadArgs& a, int32_t x_dtype, int32_t dy_dtype, int32_t 
   }
   return true;
 }
+
+// Entries of a unit's vectors: 16 bytes of the widest type.
+template <typename... T>
+constexpr int vector_width = (std::is_same_v<T, float> || ...) ? 4 : 8;
 
 template <typename F>
 cudaError_t with_group(int32_t d, F f) {
@@ -619,7 +645,7 @@ cudaError_t launch_heads_vec(const HeadArgs& a, int32_t x_dtype, int32_t y_dtype
     }
     // full rounds for the smallest set and at least kRounds of them in all, where the
     // batch has the tokens; small batches spread over the SMs instead
-    constexpr int kGroups = kThreadsVec / G, kRounds = 8;
+    constexpr int kGroups = kThreadsVec / G, kRounds = 4;
     const int64_t want = std::max<int64_t>((kGroups + fewest - 1) / fewest, (kRounds * kGroups + heads - 1) / heads);
     const int32_t tokens =
         static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({want, 32, a.total / (2 * 148)})));
@@ -629,7 +655,7 @@ cudaError_t launch_heads_vec(const HeadArgs& a, int32_t x_dtype, int32_t y_dtype
     const Quotients q = quotients(a, each);
     return with_type(x_dtype, [&](auto ti) {
       return with_type(y_dtype, [&](auto to) {
-        heads_vec_kernel<decltype(ti), decltype(to), G><<<blocks, kThreadsVec, smem, stream>>>(a, q, tokens);
+        heads_vec_kernel<decltype(ti), decltype(to), vector_width<decltype(ti), decltype(to)>, G><<<blocks, kThreadsVec, smem, stream>>>(a, q, tokens);
         return cudaGetLastError();
       });
     });
@@ -688,7 +714,7 @@ cudaError_t launch_head_grads_vec(const HeadArgs& a, int32_t x_dtype, int32_t dy
           using TI = decltype(ti);
           using TG = decltype(tg);
           using TO = decltype(to);
-          auto* kernel = head_grads_vec_kernel<TI, TG, TO, G>;
+          auto* kernel = head_grads_vec_kernel<TI, TG, TO, vector_width<TI, TG, TO>, G>;
           if (smem > 48 * 1024) {
             const cudaError_t e =
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
