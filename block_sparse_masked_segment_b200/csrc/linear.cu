@@ -5,6 +5,7 @@
 // 16-bit operands, fp32 sums, each output rounded once.
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 
 #include "attn_common.cuh"
 #include "host_status.h"
@@ -94,7 +95,7 @@ struct ProductArgs {
   int32_t rows_q;
   int64_t depth;
   int32_t f16;
-  int32_t tiles_p, tiles_q;
+  int32_t tiles_p, tiles_q;  // product_pair_kernel
   int32_t vec;  // y, z, residual and bias allow 16-byte accesses of eight neighbours
   LinearEpilogue e;
   int32_t* dev_status;
@@ -112,6 +113,87 @@ __device__ __forceinline__ bool finish(const LinearEpilogue& e, bool f16, int64_
   return store_typed(e.y, e.y_dtype, m * e.ldy + n, z) || bad;
 }
 
+// W = 4 or 8 neighbours of a row of type dtype, aligned to W entries of 16 bits (16
+// bytes for fp32).
+template <int W>
+__device__ __forceinline__ void load_row(const void* p, int32_t dtype, int64_t i, float (&v)[W]) {
+  if (dtype == OPR_DTYPE_FP32) {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int q = 0; q < W / 4; ++q) {
+      const float4 x = f[q];
+      v[4 * q] = x.x;
+      v[4 * q + 1] = x.y;
+      v[4 * q + 2] = x.z;
+      v[4 * q + 3] = x.w;
+    }
+    return;
+  }
+  using Words = std::conditional_t<W == 8, uint4, uint2>;
+  const Words u = *reinterpret_cast<const Words*>(static_cast<const uint16_t*>(p) + i);
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&u);
+#pragma unroll
+  for (int k = 0; k < W / 2; ++k) {
+    if (dtype == OPR_DTYPE_BF16) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+    }
+  }
+}
+
+template <int W>
+__device__ __forceinline__ bool store_row(void* p, int32_t dtype, int64_t i, const float (&v)[W]) {
+  if (dtype == OPR_DTYPE_FP32) {
+    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+#pragma unroll
+    for (int q = 0; q < W / 4; ++q) f[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    return false;
+  }
+  using Words = std::conditional_t<W == 8, uint4, uint2>;
+  Words u;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < W / 2; ++k) {
+    if (dtype == OPR_DTYPE_BF16) {
+      w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    } else {
+      w[k] = pack_f16x2(v[2 * k], v[2 * k + 1]);
+      bad |= !(fabsf(v[2 * k]) <= 65504.f) || !(fabsf(v[2 * k + 1]) <= 65504.f);
+    }
+  }
+  *reinterpret_cast<Words*>(static_cast<uint16_t*>(p) + i) = u;
+  return bad;
+}
+
+// W neighbouring outputs of row m (ProductArgs::vec).
+template <int W>
+__device__ __forceinline__ bool finish_row(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, float (&v)[W]) {
+  bool bad = false;
+  if (e.bias != nullptr) {
+    float b[W];
+    load_row<W>(e.bias, e.bias_dtype, n, b);
+#pragma unroll
+    for (int k = 0; k < W; ++k) v[k] += b[k];
+  }
+  if (e.z != nullptr) bad |= store_row<W>(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, v);
+  if (e.activation != OPR_ACT_NONE) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) v[k] = activate(v[k], e.activation);
+  }
+  if (e.residual != nullptr) {
+    float r[W];
+    load_row<W>(e.residual, e.residual_dtype, m * e.ld_residual + n, r);
+#pragma unroll
+    for (int k = 0; k < W; ++k) v[k] += r[k];
+  }
+  return store_row<W>(e.y, e.y_dtype, m * e.ldy + n, v) || bad;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -125,11 +207,17 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float load_peer(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
   uint32_t a;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return a;
+}
+__device__ __forceinline__ float4 load_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -141,12 +229,14 @@ __device__ __forceinline__ uint64_t depth_limit(uint64_t wait_ns, int slices) {
 
 constexpr int kProductThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
 constexpr int kProductSmem = 225 * 1024;
+constexpr int kTileSmem = 110 * 1024;  // two CTAs an SM
+constexpr int kMaxSplit = 8;
 
 template <bool Q_MN, int BN>
 struct TileSmem {
   static constexpr int kRowsQ = Q_MN && BN < 64 ? 64 : BN;  // an MN-major chunk has 64 rows
   static constexpr int kStageBytes = (kRowsP + kRowsQ) * 128;
-  static constexpr int kStages = 220 * 1024 / kStageBytes < 12 ? 220 * 1024 / kStageBytes : 12;
+  static constexpr int kStages = 108 * 1024 / kStageBytes;
   alignas(1024) uint8_t ring[kStages][kStageBytes];
   uint64_t full[kStages], empty[kStages], done;
   uint32_t tmem_base;
@@ -155,17 +245,22 @@ struct TileSmem {
 
 // One 128 x BN tile per cluster, its depth split over the cluster's CTAs.  Each CTA
 // leaves its partial tile (fp32) in its own shared memory, where the ring was; after
-// the cluster's barrier each CTA adds up and finishes every cluster-size-th line of
-// the tile, the partials in rank order (deterministic, no workspace, one launch).
-// SWAP: the lines of C are columns of y (P holds the n side, Q the m side).
+// the cluster's barrier each CTA adds up and finishes its share of the tile's lines,
+// the partials in rank order (deterministic, no workspace, one launch).  Two CTAs
+// share an SM, so that one's epilogue runs next to the other's products.
+// SWAP: P holds the n side, Q the m side.
 template <bool P_MN, bool Q_MN, int BN, bool SWAP>
-__global__ void __launch_bounds__(kProductThreads, 1)
+__global__ void __launch_bounds__(kProductThreads, 2)
     product_tile_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ ProductArgs a) {
   using Smem = TileSmem<Q_MN, BN>;
   constexpr int kRowsQ = Smem::kRowsQ;
   constexpr int kStages = Smem::kStages;
   constexpr uint32_t kCols = BN < 32 ? 32 : BN;
+  // floats from line to line of the partial tile: lines along the contiguous
+  // direction of y, 16-byte accesses without bank conflicts
+  constexpr int kLines = SWAP ? BN : kRowsP, kLine = SWAP ? kRowsP : BN, kLineLd = kLine + 4;
+  static_assert(kLines * kLineLd * 4 <= static_cast<int>(sizeof(Smem::ring)), "the partial tile fits where the ring was");
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(align1024(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -222,14 +317,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mma_commit(&sm.empty[s]);
     }
     mma_commit(&sm.done);
-    __all_sync(0xffffffffu, mbar_wait(&sm.done, 0, nullptr, kWaitLimitNs));
+    if (!warp_wait(&sm.done, 0, nullptr, kWaitLimitNs)) *abort_flag = 1;
   }
-  // the partial tile: [128][BN + 1] (lines along q) or, swapped, [BN][128] (lines along p)
-  float* part = reinterpret_cast<float*>(sm.ring);
-  const bool ok = mbar_wait(&sm.done, 0, nullptr, depth_limit(kWaitLimitNs, n));
-  __syncthreads();
-  const bool aborted = *abort_flag != 0 || !ok;
+  __syncthreads();  // the producer's copies have landed, the products are complete
+  const bool aborted = *abort_flag != 0;
   tc_fence_after();
+  float* part = reinterpret_cast<float*>(sm.ring);
   if (warp >= 2) {
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -237,80 +330,95 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (int c = half * 16; c < BN; c += 32) {
       uint32_t r[16];
       tmem_ld16(tl + c, r);
+      if constexpr (SWAP) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float v = n > 0 ? __uint_as_float(r[i]) : 0.f;
-        if constexpr (SWAP)
-          part[(c + i) * kRowsP + row] = v;
-        else
-          part[row * (BN + 1) + c + i] = v;
+        for (int i = 0; i < 16; ++i) part[(c + i) * kLineLd + row] = __uint_as_float(r[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(part + row * kLineLd + c + 4 * i) =
+              make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
       }
     }
     tc_fence_before();
   }
-  cluster_sync();
-  bool bad = false;
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // line i of the tile is row m0 + i of y, entry j of a line its column n0 + j
+  const int64_t m0 = SWAP ? q0 : p0, n0 = SWAP ? p0 : q0;
+  const int64_t rows = SWAP ? a.rows_q : a.rows_p, cols = SWAP ? a.rows_p : a.rows_q;
+  const int lines = rows - m0 < kLines ? static_cast<int>(rows - m0) : kLines;
+  const int len = cols - n0 < kLine ? static_cast<int>(cols - n0) : kLine;
   const uint32_t base = smem_u32(part);
-  if constexpr (SWAP) {
-    const int lines = a.rows_q - q0 < BN ? a.rows_q - q0 : BN;
-    for (int i = static_cast<int>(rank) + static_cast<int>(ranks) * (threadIdx.x / kRowsP); i < lines;
-         i += static_cast<int>(ranks) * 2) {
-      if (threadIdx.x >= 2 * kRowsP) break;
-      const int p = threadIdx.x % kRowsP;
-      if (p0 + p >= a.rows_p) continue;
-      float v = 0.f;
-      for (uint32_t r = 0; r < ranks; ++r) v += load_peer(base + 4 * (i * kRowsP + p), r);
-      bad |= finish(a.e, a.f16 != 0, q0 + i, p0 + p, v);
-    }
-  } else {
-    const int lines = a.rows_p - p0 < kRowsP ? static_cast<int>(a.rows_p - p0) : kRowsP;
-    for (int i = static_cast<int>(rank) + static_cast<int>(ranks) * warp; i < lines;
-         i += static_cast<int>(ranks) * (kProductThreads / 32)) {
-      for (int c = lane; c < BN; c += 32) {
-        if (q0 + c >= a.rows_q) continue;
-        float v = 0.f;
-        for (uint32_t r = 0; r < ranks; ++r) v += load_peer(base + 4 * (i * (BN + 1) + c), r);
-        bad |= finish(a.e, a.f16 != 0, p0 + i, q0 + c, v);
+  uint32_t peer[kMaxSplit];
+#pragma unroll
+  for (int r = 0; r < kMaxSplit; ++r) peer[r] = peer_addr(base, r < static_cast<int>(ranks) ? r : 0);
+  bool bad = false;
+  constexpr int kQuads = kLine / 4;  // groups of four entries of a line
+  for (int i = threadIdx.x + static_cast<int>(rank) * kProductThreads; i < lines * kQuads;
+       i += static_cast<int>(ranks) * kProductThreads) {
+    const int line = i / kQuads, j = i % kQuads * 4;
+    if (j >= len) continue;
+    const uint32_t at = 4 * (line * kLineLd + j);
+    float4 v;
+    if (ranks == 1) {
+      v = *reinterpret_cast<const float4*>(part + line * kLineLd + j);
+    } else {
+      v = load_peer4(peer[0] + at);
+#pragma unroll
+      for (int r = 1; r < kMaxSplit; ++r) {
+        if (r >= static_cast<int>(ranks)) break;
+        const float4 x = load_peer4(peer[r] + at);
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
       }
+    }
+    float f[4] = {v.x, v.y, v.z, v.w};
+    if (a.vec) {
+      bad |= finish_row<4>(a.e, a.f16 != 0, m0 + line, n0 + j, f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + k < len) bad |= finish(a.e, a.f16 != 0, m0 + line, n0 + j + k, f[k]);
     }
   }
   if (bad) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
   if (aborted && threadIdx.x == 0) atomicOr(a.dev_status, OPR_DEV_WAIT_TIMEOUT);
-  cluster_sync();  // no CTA ends while another reads its shared memory
+  if (ranks > 1) cluster_sync();  // no CTA ends while another reads its shared memory
   if (warp == 1) tmem_dealloc(tmem, kCols);
 }
 
 // ---------------------------------------------------------------- large products
-// Persistent CTA pairs: one 256 x 256 tile at a time per pair (cta_group::2), each
-// CTA staging its own 128 rows of P and its half of Q's 256 rows, so that a pair
-// reads each staged byte once where two CTAs of their own would read Q twice.  Two
+// Persistent CTA pairs: one 256 x BN tile at a time per pair (cta_group::2), each
+// CTA staging its own 128 rows of P and its half of Q's BN rows, so that a pair reads
+// each staged byte once where two CTAs of their own would read Q twice.  Two
 // accumulators: the epilogue of a tile runs while the next one is multiplied.
-constexpr int kPairStages = 5;
-constexpr int kPairTile = 256;
+constexpr int kPairRows = 256;
 constexpr int kEpiWarps = 8;
 constexpr int kStageLd = 36;  // floats from row to row of a warp's 32 x 32 staging: 16-byte accesses without conflicts
 
+template <int BN>
 struct PairSmem {
-  alignas(1024) uint8_t ring[kPairStages][2 * kRowsP * 128];
+  static constexpr int kStageBytes = (kRowsP + BN / 2) * 128;
+  static constexpr int kStages = BN == 256 ? 5 : BN == 128 ? 7 : 8;
+  alignas(1024) uint8_t ring[kStages][kStageBytes];
   alignas(16) float stage[kEpiWarps][32 * kStageLd];
-  uint64_t full[kPairStages], empty[kPairStages];  // full: the leader's, counts both CTAs' bytes
-  uint64_t acc_full[2], acc_empty[2];              // acc_empty: the leader's
+  uint64_t full[kStages], empty[kStages];  // full: the leader's, counts both CTAs' bytes
+  uint64_t acc_full[2], acc_empty[2];      // acc_empty: the leader's
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag;
   int issued;
 };
-static_assert(sizeof(PairSmem) + 1024 <= kProductSmem, "the ring and the staging fit an SM");
 
-__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-  return a;
-}
-
-// Loads 128 rows of an operand for the pair; `bar` is the leader's barrier (cluster address).
-template <bool MN>
+// Loads R rows of an operand for the pair; `bar` is the leader's barrier (cluster address).
+template <bool MN, int R>
 __device__ __forceinline__ void load_pair_slice(const CUtensorMap* map, uint32_t bar, uint8_t* dst, int row0, int k0) {
+  static_assert(!MN || R % 64 == 0, "an MN-major chunk has 64 rows");
   auto box = [&](uint8_t* to, int c0, int c1) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -319,8 +427,8 @@ __device__ __forceinline__ void load_pair_slice(const CUtensorMap* map, uint32_t
         : "memory");
   };
   if constexpr (MN) {
-    box(dst, row0, k0);
-    box(dst + kChunk, row0 + 64, k0);
+#pragma unroll
+    for (int c = 0; c < R / 64; ++c) box(dst + c * kChunk, row0 + 64 * c, k0);
   } else {
     box(dst, k0, row0);
   }
@@ -348,71 +456,6 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 
-// Eight neighbours of a row of type dtype (16-byte aligned).
-__device__ __forceinline__ void load8(const void* p, int32_t dtype, int64_t i, float (&v)[8]) {
-  if (dtype == OPR_DTYPE_FP32) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    return;
-  }
-  const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (dtype == OPR_DTYPE_BF16) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-      v[2 * k] = f.x;
-      v[2 * k + 1] = f.y;
-    }
-  }
-}
-
-__device__ __forceinline__ bool store8(void* p, int32_t dtype, int64_t i, const float (&v)[8]) {
-  if (dtype == OPR_DTYPE_FP32) {
-    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    f[0] = make_float4(v[0], v[1], v[2], v[3]);
-    f[1] = make_float4(v[4], v[5], v[6], v[7]);
-    return false;
-  }
-  uint4 u;
-  bool bad = false;
-  if (dtype == OPR_DTYPE_BF16) {
-    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  } else {
-    u = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) bad |= !(fabsf(v[k]) <= 65504.f);
-  }
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = u;
-  return bad;
-}
-
-__device__ __forceinline__ bool finish8(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, float (&v)[8]) {
-  bool bad = false;
-  if (e.bias != nullptr) {
-    float b[8];
-    load8(e.bias, e.bias_dtype, n, b);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += b[k];
-  }
-  if (e.z != nullptr) bad |= store8(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, v);
-  if (e.activation != OPR_ACT_NONE) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = activate(v[k], e.activation);
-  }
-  if (e.residual != nullptr) {
-    float r[8];
-    load8(e.residual, e.residual_dtype, m * e.ld_residual + n, r);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += r[k];
-  }
-  return store8(e.y, e.y_dtype, m * e.ldy + n, v) || bad;
-}
-
 // Tile t of the walk: groups of kGroup tile rows, columns outer inside a group, so
 // that the pairs that run together share rows of P and Q in L2.
 constexpr int kGroup = 8;
@@ -424,12 +467,14 @@ __device__ __forceinline__ void tile_at(int t, int tiles_p, int tiles_q, int& tp
   tq = r / rows;
 }
 
-template <bool P_MN, bool Q_MN>
+template <bool P_MN, bool Q_MN, int BN>
 __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ ProductArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  PairSmem& sm = *reinterpret_cast<PairSmem*>(align1024(smem_raw));
+  using Smem = PairSmem<BN>;
+  constexpr int kStages = Smem::kStages;
+  Smem& sm = *reinterpret_cast<Smem*>(align1024(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int slices = static_cast<int>((a.depth + kDepth - 1) / kDepth);
@@ -437,7 +482,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
   const int pairs = gridDim.x / 2, first = blockIdx.x / 2;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
@@ -464,13 +509,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
   volatile int* abort_flag = &sm.abort_flag;
 
   auto fill = [&](int j, int tp, int tq, int slice) {
-    const int s = j % kPairStages;
+    const int s = j % kStages;
     // the leader's barrier counts both CTAs' bytes of the stage
-    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 4 * kRowsP * 128);
+    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Smem::kStageBytes);
     const uint32_t bar = peer_addr(smem_u32(&sm.full[s]), 0);
-    load_pair_slice<P_MN>(&map_p, bar, sm.ring[s], tp * kPairTile + static_cast<int>(rank) * kRowsP, slice * kDepth);
-    load_pair_slice<Q_MN>(&map_q, bar, sm.ring[s] + kRowsP * 128, tq * kPairTile + static_cast<int>(rank) * kRowsP,
-                          slice * kDepth);
+    load_pair_slice<P_MN, kRowsP>(&map_p, bar, sm.ring[s], tp * kPairRows + static_cast<int>(rank) * kRowsP, slice * kDepth);
+    load_pair_slice<Q_MN, BN / 2>(&map_q, bar, sm.ring[s] + kRowsP * 128, tq * BN + static_cast<int>(rank) * (BN / 2),
+                                  slice * kDepth);
   };
 
   if (warp == 0) {
@@ -481,8 +526,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
         int tp, tq;
         tile_at(t, a.tiles_p, a.tiles_q, tp, tq);
         for (int k = 0; k < slices; ++k, ++j) {
-          if (j >= kPairStages &&
-              !mbar_wait(&sm.empty[j % kPairStages], ((j / kPairStages) + 1) & 1, abort_flag, a.wait_ns)) {
+          if (j >= kStages &&
+              !mbar_wait(&sm.empty[j % kStages], ((j / kStages) + 1) & 1, abort_flag, a.wait_ns)) {
             ok = false;
             break;
           }
@@ -491,12 +536,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
       }
       sm.issued = j;
       // the releases of the last stages, which the leader's MMAs send here
-      for (int u = j > kPairStages ? j - kPairStages : 0; ok && u < j; ++u)
-        ok = mbar_wait(&sm.empty[u % kPairStages], (u / kPairStages) & 1, abort_flag, a.wait_ns);
+      for (int u = j > kStages ? j - kStages : 0; ok && u < j; ++u)
+        ok = mbar_wait(&sm.empty[u % kStages], (u / kStages) & 1, abort_flag, a.wait_ns);
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      const uint32_t idesc = idesc_f32acc(kPairTile, kPairTile, a.f16 != 0, P_MN, Q_MN);
+      const uint32_t idesc = idesc_f32acc(kPairRows, BN, a.f16 != 0, P_MN, Q_MN);
       int j = 0, i = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += pairs, ++i) {
@@ -504,15 +549,15 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
         if (i >= 2) ok = warp_wait(&sm.acc_empty[b], ((i >> 1) + 1) & 1, abort_flag, a.wait_ns);
         tc_fence_after();
         for (int k = 0; ok && k < slices; ++k, ++j) {
-          const int s = j % kPairStages;
-          ok = warp_wait(&sm.full[s], (j / kPairStages) & 1, abort_flag, a.wait_ns);
+          const int s = j % kStages;
+          ok = warp_wait(&sm.full[s], (j / kStages) & 1, abort_flag, a.wait_ns);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sa = smem_u32(sm.ring[s]);
           const uint64_t dp = slice_desc<P_MN>(sa), dq = slice_desc<Q_MN>(sa + kRowsP * 128);
 #pragma unroll
           for (int kk = 0; kk < kDepth / 16; ++kk)
-            mma_pair(tmem + b * kPairTile, dp + slice_step<P_MN>(kk), dq + slice_step<Q_MN>(kk), idesc,
+            mma_pair(tmem + b * BN, dp + slice_step<P_MN>(kk), dq + slice_step<Q_MN>(kk), idesc,
                      (k | kk) != 0 ? 1u : 0u);
           commit_pair(&sm.empty[s]);
         }
@@ -527,7 +572,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
           "@E tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
               smem_u32(&sm.done))
           : "memory");
-      __all_sync(0xffffffffu, mbar_wait(&sm.done, 0, nullptr, kWaitLimitNs));
+      if (!warp_wait(&sm.done, 0, nullptr, kWaitLimitNs)) *abort_flag = 1;
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
@@ -543,19 +588,20 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
       tile_at(t, a.tiles_p, a.tiles_q, tp, tq);
       if (!warp_wait(&sm.acc_full[b], (i >> 1) & 1, abort_flag, depth_limit(a.wait_ns, slices))) break;
       tc_fence_after();
-      const int64_t m0 = static_cast<int64_t>(tp) * kPairTile + rank * kRowsP + quad * 32;
-      for (int c = 0; c < 4; ++c) {
-        const int col = half * 128 + c * 32;
+      const int64_t m0 = static_cast<int64_t>(tp) * kPairRows + rank * kRowsP + quad * 32;
+      constexpr int kChunks = BN / 64;  // of 32 columns, for this warp
+      for (int c = 0; c < kChunks; ++c) {
+        const int col = half * (BN / 2) + c * 32;
         uint32_t r[32];
-        tmem_ld32(tl + b * kPairTile + col, r);
-        if (c == 3) {  // this warp has read its part of the accumulator
+        tmem_ld32(tl + b * BN + col, r);
+        if (c == kChunks - 1) {  // this warp has read its part of the accumulator
           tc_fence_before();
           if (lane == 0)
             asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                              peer_addr(smem_u32(&sm.acc_empty[b]), 0))
                          : "memory");
         }
-        const int64_t n0 = static_cast<int64_t>(tq) * kPairTile + col;
+        const int64_t n0 = static_cast<int64_t>(tq) * BN + col;
         if (m0 >= a.rows_p || n0 >= a.rows_q) continue;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -572,7 +618,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
             const float4* f = reinterpret_cast<const float4*>(stage + row * kStageLd + (lane & 3) * 8);
             const float4 x = f[0], y = f[1];
             v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-            bad |= finish8(e, f16, m0 + row, n, v);
+            bad |= finish_row<8>(e, f16, m0 + row, n, v);
           }
         } else if (n0 + lane < a.rows_q) {
           for (int row = 0; row < 32 && m0 + row < a.rows_p; ++row)
@@ -595,14 +641,22 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     const int upto = mine > theirs ? mine : theirs;
     for (int j = mine; j < upto; ++j) fill(j, 0, 0, 0);
     if (rank == 0)
-      for (int j = upto > kPairStages ? upto - kPairStages : 0; j < upto; ++j)
-        mbar_wait(&sm.full[j % kPairStages], (j / kPairStages) & 1, nullptr, kWaitLimitNs);
+      for (int j = upto > kStages ? upto - kStages : 0; j < upto; ++j)
+        mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, nullptr, kWaitLimitNs);
     if (*abort_flag != 0) atomicOr(a.dev_status, OPR_DEV_WAIT_TIMEOUT);
   }
   __syncthreads();
   cluster_sync();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// Nothing to add up (the gradient of a weight over no rows): the epilogue of zeros.
+__global__ void __launch_bounds__(256) no_depth_kernel(const __grid_constant__ ProductArgs a) {
+  const int64_t n = a.rows_p * a.rows_q;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    finish(a.e, a.f16 != 0, i / a.rows_q, i % a.rows_q, 0.f);
 }
 
 // A matrix whose rows start off the 16-byte grid, copied to rows that start on it.
@@ -666,39 +720,54 @@ bool operand_map(CUtensorMap* map, const Operand& o, int64_t rows, int64_t depth
                       const_cast<void*>(o.p), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Lets a kernel use kProductSmem of shared memory, once per device and kernel.
+// Lets a kernel use `bytes` of shared memory, once per device and kernel.
 template <auto* kKernel>
-cudaError_t allow_smem() {
+cudaError_t allow_smem(int bytes) {
   static std::atomic<uint64_t> allowed{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t{1} << (dev & 63);
   if (dev < 64 && (allowed.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
-  if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
 
+bool vector_epilogue(const LinearEpilogue& e, int64_t n) {
+  auto fits = [](const void* p, int64_t ld) {
+    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0);
+  };
+  return n % 8 == 0 && fits(e.y, e.ldy) && fits(e.z, e.ldz) && fits(e.residual, e.ld_residual) && fits(e.bias, 0);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// CTAs of two to an SM that run at one time in clusters of 1 .. 8 (B200: 148 SMs,
+// the clusters within its GPCs; as the occupancy query reports them).
+constexpr int kSlots[kMaxSplit] = {296, 296, 279, 284, 280, 270, 259, 264};
+
 template <bool P_MN, bool Q_MN, int BN, bool SWAP>
-cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, int split, cudaStream_t stream) {
+cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
   CUtensorMap mp, mq;
-  // with nothing to add up no box is loaded, and the maps (of valid extents) are not used
-  const int64_t depth = a.depth > 0 ? a.depth : 1;
-  if (!operand_map(&mp, p, a.rows_p, depth, a.f16 != 0, kRowsP) ||
-      !operand_map(&mq, q, a.rows_q, depth, a.f16 != 0, BN))
+  if (!operand_map(&mp, p, a.rows_p, a.depth, a.f16 != 0, kRowsP) ||
+      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, BN))
     return cudaErrorInvalidValue;
   constexpr auto* kernel = product_tile_kernel<P_MN, Q_MN, BN, SWAP>;
-  using Smem = TileSmem<Q_MN, BN>;
-  static_assert(sizeof(Smem) + 1024 <= kProductSmem, "a tile's ring fits an SM");
-  static_assert((SWAP ? BN * kRowsP : kRowsP * (BN + 1)) * 4 <= static_cast<int>(sizeof(Smem::ring)),
-                "the partial tile fits where the ring was");
-  const cudaError_t e = allow_smem<kernel>();
+  static_assert(sizeof(TileSmem<Q_MN, BN>) + 1024 <= kTileSmem, "a tile's ring fits half an SM");
+  const cudaError_t e = allow_smem<kernel>(kTileSmem);
   if (e != cudaSuccess) return e;
+  const int64_t tiles_p = ceil_div(a.rows_p, kRowsP), tiles_q = ceil_div(a.rows_q, BN), tiles = tiles_p * tiles_q;
+  const int64_t slices = ceil_div(a.depth, kDepth);
+  // the depth split over as many CTAs as run at one time, four slices or more to each
+  int split = 1;
+  for (int c = 2; c <= kMaxSplit; ++c)
+    if (tiles * c <= kSlots[c - 1] && slices >= 4 * c) split = c;
+  a.vec = vector_epilogue(a.e, SWAP ? a.rows_p : a.rows_q);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.tiles_p * split), static_cast<unsigned>(a.tiles_q));
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles_p * split), static_cast<unsigned>(tiles_q));
   cfg.blockDim = dim3(kProductThreads);
-  cfg.dynamicSmemBytes = kProductSmem;
+  cfg.dynamicSmemBytes = kTileSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -708,49 +777,39 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, int 
   return cudaLaunchKernelEx(&cfg, kernel, mp, mq, a);
 }
 
-bool vector_epilogue(const LinearEpilogue& e, int32_t n) {
-  auto fits = [](const void* p, int64_t ld) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0); };
-  return n % 8 == 0 && fits(e.y, e.ldy) && fits(e.z, e.ldz) && fits(e.residual, e.ld_residual) && fits(e.bias, 0);
-}
-
-template <bool P_MN, bool Q_MN>
+template <bool P_MN, bool Q_MN, int BN>
 cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
   CUtensorMap mp, mq;
   if (!operand_map(&mp, p, a.rows_p, a.depth, a.f16 != 0, kRowsP) ||
-      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, kRowsP))
+      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, BN / 2))
     return cudaErrorInvalidValue;
-  constexpr auto* kernel = product_pair_kernel<P_MN, Q_MN>;
-  const cudaError_t e = allow_smem<kernel>();
+  constexpr auto* kernel = product_pair_kernel<P_MN, Q_MN, BN>;
+  static_assert(sizeof(PairSmem<BN>) + 1024 <= kProductSmem, "the ring and the staging fit an SM");
+  const cudaError_t e = allow_smem<kernel>(kProductSmem);
   if (e != cudaSuccess) return e;
-  a.tiles_p = static_cast<int32_t>((a.rows_p + kPairTile - 1) / kPairTile);
-  a.tiles_q = (a.rows_q + kPairTile - 1) / kPairTile;
+  a.tiles_p = static_cast<int32_t>(ceil_div(a.rows_p, kPairRows));
+  a.tiles_q = static_cast<int32_t>(ceil_div(a.rows_q, BN));
   a.vec = vector_epilogue(a.e, a.rows_q);
   const int64_t pairs = std::min<int64_t>(static_cast<int64_t>(a.tiles_p) * a.tiles_q, 148 / 2);
   kernel<<<static_cast<unsigned>(2 * pairs), kProductThreads, kProductSmem, stream>>>(mp, mq, a);
   return cudaGetLastError();
 }
 
-// A launch of single tiles: the depth of each split over as many CTAs of a cluster
-// as fill the 148 SMs once, four slices or more to each.
-template <bool P_MN, bool Q_MN, int BN, bool SWAP>
-cudaError_t launch_split_tiles(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
-  a.tiles_p = static_cast<int32_t>((a.rows_p + kRowsP - 1) / kRowsP);
-  a.tiles_q = (a.rows_q + BN - 1) / BN;
-  const int64_t tiles = static_cast<int64_t>(a.tiles_p) * a.tiles_q;
-  const int64_t slices = (a.depth + kDepth - 1) / kDepth;
-  const int64_t split = std::max<int64_t>(1, std::min<int64_t>({8, 148 / tiles, slices / 4}));
-  return launch_tiles<P_MN, Q_MN, BN, SWAP>(p, q, a, static_cast<int>(split), stream);
-}
-
 template <bool P_MN, bool Q_MN>
 cudaError_t launch_product(const Operand& p, const Operand& q, const ProductArgs& a, cudaStream_t stream) {
-  auto tiles = [&](int bn) { return (a.rows_p + kRowsP - 1) / kRowsP * ((a.rows_q + bn - 1) / bn); };
-  const int64_t pair_tiles =
-      (a.rows_p + kPairTile - 1) / kPairTile * ((a.rows_q + kPairTile - 1) / kPairTile);
-  if (a.depth > 0 && pair_tiles >= 74 && pair_tiles < (int64_t{1} << 30)) return launch_pairs<P_MN, Q_MN>(p, q, a, stream);
-  if (tiles(256) >= 148) return launch_split_tiles<P_MN, Q_MN, 256, false>(p, q, a, stream);
-  if (tiles(128) >= 148) return launch_split_tiles<P_MN, Q_MN, 128, false>(p, q, a, stream);
-  return launch_split_tiles<P_MN, Q_MN, 64, false>(p, q, a, stream);
+  auto pairs = [&](int bn) { return ceil_div(a.rows_p, kPairRows) * ceil_div(a.rows_q, bn); };
+  if (const char* f = getenv("LINF")) {
+    switch (atoi(f)) {
+      case 1: return launch_pairs<P_MN, Q_MN, 256>(p, q, a, stream);
+      case 2: return launch_pairs<P_MN, Q_MN, 128>(p, q, a, stream);
+      case 3: if constexpr (!Q_MN) return launch_pairs<P_MN, Q_MN, 64>(p, q, a, stream);
+      case 4: return launch_tiles<P_MN, Q_MN, 128, false>(p, q, a, stream);
+      case 5: return launch_tiles<P_MN, Q_MN, 64, false>(p, q, a, stream);
+    }
+  }
+  if (pairs(256) >= 74) return launch_pairs<P_MN, Q_MN, 256>(p, q, a, stream);
+  if (pairs(128) >= 48) return launch_pairs<P_MN, Q_MN, 128>(p, q, a, stream);
+  return launch_tiles<P_MN, Q_MN, 64, false>(p, q, a, stream);
 }
 
 // Few rows of x: the weight fills the tiles' 128 rows, the rows of x their columns.
@@ -759,8 +818,8 @@ cudaError_t launch_few_rows(const Operand& x, const Operand& w, ProductArgs a, c
   const int64_t m = a.rows_p;
   a.rows_p = a.rows_q;
   a.rows_q = static_cast<int32_t>(m);
-  if (m <= 16) return launch_split_tiles<W_MN, false, 16, true>(w, x, a, stream);
-  return launch_split_tiles<W_MN, false, 64, true>(w, x, a, stream);
+  if (m <= 16) return launch_tiles<W_MN, false, 16, true>(w, x, a, stream);
+  return launch_tiles<W_MN, false, 64, true>(w, x, a, stream);
 }
 constexpr int64_t kFewRows = 64;
 
@@ -777,6 +836,10 @@ cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t m, int32_t
   args.e = e;
   args.dev_status = dev_status;
   args.wait_ns = wait_limit_ns();
+  if (k == 0) {
+    no_depth_kernel<<<static_cast<unsigned>(std::min<int64_t>((m * n + 255) / 256, 148 * 16)), 256, 0, stream>>>(args);
+    return cudaGetLastError();
+  }
   const bool a_mn = a.col != 1, b_mn = b.col != 1;
   if (a_mn) return launch_product<true, true>(a, b, args, stream);
   if (m <= kFewRows) return b_mn ? launch_few_rows<true>(a, b, args, stream) : launch_few_rows<false>(a, b, args, stream);

@@ -187,11 +187,14 @@ def test_linear_gradients_in_fp32():
     within(dw, to64(dy).T @ to64(x), sum_bound(to64(dy).T, to64(x).T, m), "fp32")
 
 
-def test_linear_of_no_rows():
-    x, w = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(40, 64, dtype=torch.bfloat16, device="cuda")
-    assert opr.opr_linear(x, w).shape == (0, 40)
-    dx, dw, db = opr.opr_linear_bwd(torch.empty(0, 40, dtype=torch.bfloat16, device="cuda"), x, w, bias=True)
-    assert dx.shape == (0, 64) and (dw == 0).all() and (db == 0).all() and dw.shape == (40, 64)
+@pytest.mark.parametrize("n,k", [(40, 64), (3, 7), (1, 1)])
+def test_linear_of_no_rows(n, k):
+    x, w = torch.empty(0, k, dtype=torch.bfloat16, device="cuda"), torch.ones(n, k, dtype=torch.bfloat16, device="cuda")
+    assert opr.opr_linear(x, w).shape == (0, n)
+    dy = torch.empty(0, n, dtype=torch.bfloat16, device="cuda")
+    for z, act in ((None, None), (dy, "silu")):
+        dx, dw, db = opr.opr_linear_bwd(dy, x, w, z, act, bias=True)
+        assert dx.shape == (0, k) and (dw == 0).all() and (db == 0).all() and dw.shape == (n, k)
 
 
 def test_linear_refusals_of_tensors():
