@@ -117,13 +117,20 @@ struct Operand {
 
 cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t m, int32_t n, int64_t k, int32_t dtype,
                           const LinearEpilogue& e, int32_t* dev_status, cudaStream_t stream);
-// Both operands' rows (columns, where `col` is the row length) start on 16-byte boundaries.
-// Copies a 16-bit matrix to rows of `ld` entries.
-cudaError_t launch_pack(const Operand& from, int64_t rows, int64_t cols, void* to, int64_t ld, cudaStream_t stream);
+// A 16-bit matrix to be copied to rows of ld_to entries (a multiple of eight; the
+// entries past `cols` of a row's last eight are written as zeros); from null: none.
+struct PackJob {
+  const void* from;
+  int64_t ld_from;
+  void* to;
+  int64_t ld_to, rows;
+  int32_t cols;
+};
+cudaError_t launch_pack(const PackJob (&jobs)[2], cudaStream_t stream);
 cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int64_t ldz, int32_t dtype, int64_t m,
                              int32_t n, int32_t activation, void* dz, int64_t ld_dz, float* db, float* partial,
                              int32_t* dev_status, cudaStream_t stream);
-// Row blocks of the dz pass, which sizes its partial column sums.
-int32_t linear_dz_blocks(int64_t m);
+// Row blocks of the dz pass at most, which sizes its partial column sums.
+int32_t linear_dz_blocks(int64_t m, int32_t n);
 
 }  // namespace opr

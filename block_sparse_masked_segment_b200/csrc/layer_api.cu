@@ -93,11 +93,11 @@ size_t copy_bytes(int64_t rows, int64_t cols) {
   return align_up(static_cast<size_t>(rows) * static_cast<size_t>(padded(cols)) * 2, 256);
 }
 
-// Copies an operand's rows to `to` with padded rows and points the operand there.
-cudaError_t pack(Operand& o, int64_t rows, int64_t cols, void* to, cudaStream_t stream) {
-  const cudaError_t e = launch_pack(o, rows, cols, to, padded(cols), stream);
+// Points an operand at a copy with padded rows, and says what to copy.
+PackJob pack(Operand& o, int64_t rows, int32_t cols, void* to) {
+  const PackJob job{o.p, o.row, to, padded(cols), rows, cols};
   o = Operand{to, padded(cols), 1};
-  return e;
+  return job;
 }
 
 bool linear_sizes_ok(int64_t m, int32_t n, int32_t k) { return m >= 0 && m < kMaxRows && n > 0 && k > 0; }
@@ -355,11 +355,13 @@ opr_status opr_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Operand ox{x, ldx, 1}, ow{w, ldw, 1};
   char* to = static_cast<char*>(workspace);
+  PackJob jobs[2] = {};
   if (!tma_ready(x, ldx)) {
-    st = status_of(pack(ox, m, k, to, s));
+    jobs[0] = pack(ox, m, k, to);
     to += copy_bytes(m, k);
   }
-  if (st == OPR_OK && !tma_ready(w, ldw)) st = status_of(pack(ow, n, k, to, s));
+  if (!tma_ready(w, ldw)) jobs[1] = pack(ow, n, k, to);
+  st = status_of(launch_pack(jobs, s));
   if (st != OPR_OK) return st;
   LinearEpilogue e{bias, bias_dtype, activation, residual, ld_residual, residual_dtype, y, ldy, y_dtype, z, ldz};
   return status_of(launch_linear(ox, ow, m, n, k, dtype, e, dev_status, s));
@@ -379,7 +381,7 @@ LinearBwdWs linear_bwd_ws(const void* dy, int64_t ld_dy, const void* x, int64_t 
   s.x = s.own_dz ? copy_bytes(m, n) : 0;
   s.w = s.x + (tma_ready(x, ldx) ? 0 : copy_bytes(m, k));
   s.partial = s.w + (tma_ready(w, ldw) ? 0 : copy_bytes(n, k));
-  s.bytes = s.partial + align_up(static_cast<size_t>(linear_dz_blocks(m)) * static_cast<size_t>(n) * sizeof(float), 256);
+  s.bytes = s.partial + align_up(static_cast<size_t>(linear_dz_blocks(m, n)) * static_cast<size_t>(n) * sizeof(float), 256);
   return s;
 }
 }  // namespace
@@ -444,8 +446,10 @@ opr_status opr_linear_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t 
     if (st != OPR_OK) return st;
   }
   Operand ox{x, ldx, 1}, ow{w, ldw, 1};
-  if (dw && m > 0 && !tma_ready(x, ldx)) st = status_of(pack(ox, m, k, wsp + ws.x, s));
-  if (st == OPR_OK && dx && m > 0 && !tma_ready(w, ldw)) st = status_of(pack(ow, n, k, wsp + ws.w, s));
+  PackJob jobs[2] = {};
+  if (dw && m > 0 && !tma_ready(x, ldx)) jobs[0] = pack(ox, m, k, wsp + ws.x);
+  if (dx && m > 0 && !tma_ready(w, ldw)) jobs[1] = pack(ow, n, k, wsp + ws.w);
+  st = status_of(launch_pack(jobs, s));
   if (st != OPR_OK) return st;
   if (dx) {
     LinearEpilogue e{};

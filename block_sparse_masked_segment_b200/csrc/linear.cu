@@ -5,7 +5,6 @@
 // 16-bit operands, fp32 sums, each output rounded once.
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
 
 #include "attn_common.cuh"
 #include "host_status.h"
@@ -170,28 +169,46 @@ __device__ __forceinline__ bool store_row(void* p, int32_t dtype, int64_t i, con
   return bad;
 }
 
-// W neighbouring outputs of row m (ProductArgs::vec).
 template <int W>
-__device__ __forceinline__ bool finish_row(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, float (&v)[W]) {
+__device__ __forceinline__ void activate_row(float (&v)[W], int32_t act) {
+  if (act == OPR_ACT_NONE) return;
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) v[k] = f(v[k]);
+  };
+  if (act == OPR_ACT_SILU)
+    each([](float z) { return activate(z, OPR_ACT_SILU); });
+  else if (act == OPR_ACT_GELU)
+    each([](float z) { return activate(z, OPR_ACT_GELU); });
+  else
+    each([](float z) { return activate(z, OPR_ACT_GELU_TANH); });
+}
+
+// W neighbouring outputs of row m (ProductArgs::vec), their bias and residual given.
+template <int W>
+__device__ __forceinline__ bool finish_row(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, float (&v)[W],
+                                           const float (&bias)[W], const float (&residual)[W]) {
   bool bad = false;
-  if (e.bias != nullptr) {
-    float b[W];
-    load_row<W>(e.bias, e.bias_dtype, n, b);
 #pragma unroll
-    for (int k = 0; k < W; ++k) v[k] += b[k];
-  }
+  for (int k = 0; k < W; ++k) v[k] += bias[k];
   if (e.z != nullptr) bad |= store_row<W>(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, v);
-  if (e.activation != OPR_ACT_NONE) {
+  activate_row<W>(v, e.activation);
 #pragma unroll
-    for (int k = 0; k < W; ++k) v[k] = activate(v[k], e.activation);
-  }
-  if (e.residual != nullptr) {
-    float r[W];
-    load_row<W>(e.residual, e.residual_dtype, m * e.ld_residual + n, r);
-#pragma unroll
-    for (int k = 0; k < W; ++k) v[k] += r[k];
-  }
+  for (int k = 0; k < W; ++k) v[k] += residual[k];
   return store_row<W>(e.y, e.y_dtype, m * e.ldy + n, v) || bad;
+}
+
+template <int W>
+__device__ __forceinline__ void load_bias(const LinearEpilogue& e, int64_t n, float (&v)[W]) {
+#pragma unroll
+  for (int k = 0; k < W; ++k) v[k] = 0.f;
+  if (e.bias != nullptr) load_row<W>(e.bias, e.bias_dtype, n, v);
+}
+template <int W>
+__device__ __forceinline__ void load_residual(const LinearEpilogue& e, int64_t m, int64_t n, float (&v)[W]) {
+#pragma unroll
+  for (int k = 0; k < W; ++k) v[k] = 0.f;
+  if (e.residual != nullptr) load_row<W>(e.residual, e.residual_dtype, m * e.ld_residual + n, v);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -272,6 +289,8 @@ __global__ void __launch_bounds__(kProductThreads, 2)
   const int n = s1 - s0;
 
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&map_p);
+    tma_prefetch_desc(&map_q);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
@@ -362,6 +381,11 @@ __global__ void __launch_bounds__(kProductThreads, 2)
     const int line = i / kQuads, j = i % kQuads * 4;
     if (j >= len) continue;
     const uint32_t at = 4 * (line * kLineLd + j);
+    float bias[4], residual[4];
+    if (a.vec) {
+      load_bias<4>(a.e, n0 + j, bias);
+      load_residual<4>(a.e, m0 + line, n0 + j, residual);
+    }
     float4 v;
     if (ranks == 1) {
       v = *reinterpret_cast<const float4*>(part + line * kLineLd + j);
@@ -379,7 +403,7 @@ __global__ void __launch_bounds__(kProductThreads, 2)
     }
     float f[4] = {v.x, v.y, v.z, v.w};
     if (a.vec) {
-      bad |= finish_row<4>(a.e, a.f16 != 0, m0 + line, n0 + j, f);
+      bad |= finish_row<4>(a.e, a.f16 != 0, m0 + line, n0 + j, f, bias, residual);
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -393,18 +417,19 @@ __global__ void __launch_bounds__(kProductThreads, 2)
 }
 
 // ---------------------------------------------------------------- large products
-// Persistent CTA pairs: one 256 x BN tile at a time per pair (cta_group::2), each
-// CTA staging its own 128 rows of P and its half of Q's BN rows, so that a pair reads
-// each staged byte once where two CTAs of their own would read Q twice.  Two
-// accumulators: the epilogue of a tile runs while the next one is multiplied.
-constexpr int kPairRows = 256;
+// Persistent CTA pairs: one 256 x 256 tile at a time per pair (cta_group::2), each
+// CTA staging its own 128 rows of P and 128 of Q, so that a pair reads each staged
+// byte once where two CTAs of their own would read Q twice (what the SMs can fetch
+// from L2, about 50 bytes a clock each, is the bound: tiles of 256 x 128 and 256 x 64
+// were never the fastest).  Two accumulators: the epilogue of a tile runs while the
+// next one is multiplied.
+constexpr int kPairTile = 256;
 constexpr int kEpiWarps = 8;
 constexpr int kStageLd = 36;  // floats from row to row of a warp's 32 x 32 staging: 16-byte accesses without conflicts
 
-template <int BN>
 struct PairSmem {
-  static constexpr int kStageBytes = (kRowsP + BN / 2) * 128;
-  static constexpr int kStages = BN == 256 ? 5 : BN == 128 ? 7 : 8;
+  static constexpr int kStageBytes = 2 * kRowsP * 128;
+  static constexpr int kStages = 5;
   alignas(1024) uint8_t ring[kStages][kStageBytes];
   alignas(16) float stage[kEpiWarps][32 * kStageLd];
   uint64_t full[kStages], empty[kStages];  // full: the leader's, counts both CTAs' bytes
@@ -414,11 +439,11 @@ struct PairSmem {
   int abort_flag;
   int issued;
 };
+static_assert(sizeof(PairSmem) + 1024 <= kProductSmem, "the ring and the staging fit an SM");
 
-// Loads R rows of an operand for the pair; `bar` is the leader's barrier (cluster address).
-template <bool MN, int R>
+// Loads 128 rows of an operand for the pair; `bar` is the leader's barrier (cluster address).
+template <bool MN>
 __device__ __forceinline__ void load_pair_slice(const CUtensorMap* map, uint32_t bar, uint8_t* dst, int row0, int k0) {
-  static_assert(!MN || R % 64 == 0, "an MN-major chunk has 64 rows");
   auto box = [&](uint8_t* to, int c0, int c1) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -428,7 +453,7 @@ __device__ __forceinline__ void load_pair_slice(const CUtensorMap* map, uint32_t
   };
   if constexpr (MN) {
 #pragma unroll
-    for (int c = 0; c < R / 64; ++c) box(dst + c * kChunk, row0 + 64 * c, k0);
+    for (int c = 0; c < kRowsP / 64; ++c) box(dst + c * kChunk, row0 + 64 * c, k0);
   } else {
     box(dst, k0, row0);
   }
@@ -467,13 +492,13 @@ __device__ __forceinline__ void tile_at(int t, int tiles_p, int tiles_q, int& tp
   tq = r / rows;
 }
 
-template <bool P_MN, bool Q_MN, int BN>
+template <bool P_MN, bool Q_MN>
 __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ ProductArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  using Smem = PairSmem<BN>;
-  constexpr int kStages = Smem::kStages;
+  using Smem = PairSmem;
+  constexpr int kStages = Smem::kStages, BN = kPairTile;
   Smem& sm = *reinterpret_cast<Smem*>(align1024(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -482,6 +507,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
   const int pairs = gridDim.x / 2, first = blockIdx.x / 2;
 
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&map_p);
+    tma_prefetch_desc(&map_q);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
@@ -513,9 +540,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     // the leader's barrier counts both CTAs' bytes of the stage
     if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Smem::kStageBytes);
     const uint32_t bar = peer_addr(smem_u32(&sm.full[s]), 0);
-    load_pair_slice<P_MN, kRowsP>(&map_p, bar, sm.ring[s], tp * kPairRows + static_cast<int>(rank) * kRowsP, slice * kDepth);
-    load_pair_slice<Q_MN, BN / 2>(&map_q, bar, sm.ring[s] + kRowsP * 128, tq * BN + static_cast<int>(rank) * (BN / 2),
-                                  slice * kDepth);
+    load_pair_slice<P_MN>(&map_p, bar, sm.ring[s], tp * kPairTile + static_cast<int>(rank) * kRowsP, slice * kDepth);
+    load_pair_slice<Q_MN>(&map_q, bar, sm.ring[s] + kRowsP * 128, tq * kPairTile + static_cast<int>(rank) * kRowsP,
+                          slice * kDepth);
   };
 
   if (warp == 0) {
@@ -541,7 +568,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      const uint32_t idesc = idesc_f32acc(kPairRows, BN, a.f16 != 0, P_MN, Q_MN);
+      const uint32_t idesc = idesc_f32acc(kPairTile, BN, a.f16 != 0, P_MN, Q_MN);
       int j = 0, i = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += pairs, ++i) {
@@ -588,39 +615,46 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
       tile_at(t, a.tiles_p, a.tiles_q, tp, tq);
       if (!warp_wait(&sm.acc_full[b], (i >> 1) & 1, abort_flag, depth_limit(a.wait_ns, slices))) break;
       tc_fence_after();
-      const int64_t m0 = static_cast<int64_t>(tp) * kPairRows + rank * kRowsP + quad * 32;
-      constexpr int kChunks = BN / 64;  // of 32 columns, for this warp
+      const int64_t m0 = static_cast<int64_t>(tp) * kPairTile + rank * kRowsP + quad * 32;
+      // chunks of 32 columns; rolled loops, so that the eight warps run from the
+      // instruction cache (unrolled, fetching was the longest stall)
+      constexpr int kChunks = BN / 64;
+      const uint32_t acc = tl + b * BN + half * (BN / 2);
+#pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
-        const int col = half * (BN / 2) + c * 32;
+        const int64_t n0 = static_cast<int64_t>(tq) * BN + half * (BN / 2) + c * 32;
+        const bool inside = m0 < a.rows_p && n0 < a.rows_q;
+        const int64_t n = n0 + (lane & 3) * 8;
+        const bool mine = inside && a.vec && n < a.rows_q;
+        float bias[8];
+        if (mine) load_bias<8>(e, n, bias);
         uint32_t r[32];
-        tmem_ld32(tl + b * BN + col, r);
-        if (c == kChunks - 1) {  // this warp has read its part of the accumulator
+        tmem_ld32(acc + 32 * c, r);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<uint4*>(stage + lane * kStageLd + 4 * q) =
+              make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+        if (c + 1 == kChunks) {  // this warp has read its part of the accumulator
           tc_fence_before();
           if (lane == 0)
             asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                              peer_addr(smem_u32(&sm.acc_empty[b]), 0))
                          : "memory");
         }
-        const int64_t n0 = static_cast<int64_t>(tq) * BN + col;
-        if (m0 >= a.rows_p || n0 >= a.rows_q) continue;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(stage + lane * kStageLd + 4 * q) =
-              make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
         __syncwarp();
-        if (a.vec) {
-          const int64_t n = n0 + (lane & 3) * 8;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int row = q * 8 + (lane >> 2);
-            if (m0 + row >= a.rows_p || n >= a.rows_q) continue;
-            float v[8];
+        if (mine) {
+          const int rows = a.rows_p - m0 < 32 ? static_cast<int>(a.rows_p - m0) : 32;
+#pragma unroll 1
+          for (int row = lane >> 2; row < rows; row += 8) {
+            float residual[8];
+            load_residual<8>(e, m0 + row, n, residual);
             const float4* f = reinterpret_cast<const float4*>(stage + row * kStageLd + (lane & 3) * 8);
             const float4 x = f[0], y = f[1];
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-            bad |= finish_row<8>(e, f16, m0 + row, n, v);
+            float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            bad |= finish_row<8>(e, f16, m0 + row, n, v, bias, residual);
           }
-        } else if (n0 + lane < a.rows_q) {
+        } else if (inside && !a.vec && n0 + lane < a.rows_q) {
+#pragma unroll 1
           for (int row = 0; row < 32 && m0 + row < a.rows_p; ++row)
             bad |= finish(e, f16, m0 + row, n0 + lane, stage[row * kStageLd + lane]);
         }
@@ -659,48 +693,123 @@ __global__ void __launch_bounds__(256) no_depth_kernel(const __grid_constant__ P
     finish(a.e, a.f16 != 0, i / a.rows_q, i % a.rows_q, 0.f);
 }
 
-// A matrix whose rows start off the 16-byte grid, copied to rows that start on it.
-__global__ void __launch_bounds__(256) pack_kernel(const uint16_t* __restrict__ x, int64_t ldx, int64_t rows,
-                                                   int64_t cols, uint16_t* __restrict__ y, int64_t ldy) {
-  const int64_t n = rows * cols;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
-    y[i / cols * ldy + i % cols] = x[i / cols * ldx + i % cols];
-}
-
-constexpr int kDzRows = 64;
-
-// dz = dy act'(z) (written when dz is not null) and the column sums of each
-// block's rows, taken before dz is rounded.  One column per thread.
-template <typename T>
-__global__ void __launch_bounds__(256) linear_dz_kernel(const T* dy, int64_t ld_dy, const T* z, int64_t ldz, int64_t m,
-                                                        int32_t n, int32_t act, T* dz, int64_t ld_dz, float* partial,
-                                                        int64_t rows_per_block, int32_t* dev_status) {
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (j >= n) return;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per_block;
-  const int64_t r1 = r0 + rows_per_block < m ? r0 + rows_per_block : m;
-  float sum = 0.f;
-  bool bad = false;
-  for (int64_t i = r0; i < r1; ++i) {
-    float g = as_float(dy[i * ld_dy + j]);
-    // __fmul_rn: one value for the sum and for dz, whether or not dz is wanted
-    if (act != OPR_ACT_NONE) g = __fmul_rn(g, activate_slope(as_float(z[i * ldz + j]), act));
-    sum += g;
-    if (dz != nullptr) {
-      bad |= beyond<T>(g);
-      dz[i * ld_dz + j] = from_float<T>(g);
+// Matrices whose rows start off the 16-byte grid, copied to rows that start on it: a
+// warp a row at a time, in eight-entry pieces of the copy.  The reads are single
+// entries, but neighbouring ones, which L1 gathers.
+struct PackArgs {
+  const uint16_t* x[2];
+  uint16_t* y[2];
+  int64_t ldx[2], ldy[2], rows[2];
+  int32_t cols[2];
+};
+__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < a.rows[0] + a.rows[1]; r += warps) {
+    const bool one = r < a.rows[0];
+    const int64_t row = one ? r : r - a.rows[0];
+    const uint16_t* x = one ? a.x[0] + row * a.ldx[0] : a.x[1] + row * a.ldx[1];
+    uint16_t* y = one ? a.y[0] + row * a.ldy[0] : a.y[1] + row * a.ldy[1];
+    const int cols = one ? a.cols[0] : a.cols[1];
+#pragma unroll 2
+    for (int c = 8 * lane; c < cols; c += 256) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = c + 2 * k < cols ? x[c + 2 * k] : 0, hi = c + 2 * k + 1 < cols ? x[c + 2 * k + 1] : 0;
+        w[k] = lo | hi << 16;
+      }
+      *reinterpret_cast<uint4*>(y + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  if (partial != nullptr) partial[static_cast<int64_t>(blockIdx.y) * n + j] = sum;
-  if (bad && dev_status != nullptr) atomicOr(dev_status, OPR_DEV_FP16_RANGE);
 }
 
+// dz = dy act'(z) (written when dz is not null) and the column sums of each block's
+// rows, taken before dz is rounded.  A thread takes W neighbouring columns (eight
+// where the rows allow 16-byte accesses, else one); the block's 256 threads are `wide`
+// column groups times 256 / wide rows, whose sums are added in order at the end.
+// HBM-bound: dy and z are read once, dz written once.
+constexpr int kDzThreads = 256;
+constexpr int kDzSpan = 32;      // column groups of a block
+constexpr int kDzMaxBlocks = 512;  // row blocks, which sizes the partial sums
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const T* dy, int64_t ld_dy, const T* z, int64_t ldz, int64_t m,
+                                                               int32_t n, int32_t act, T* dz, int64_t ld_dz, float* partial,
+                                                               int64_t rows_per_block, int32_t* dev_status) {
+  constexpr int32_t kType = std::is_same_v<T, __half> ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16;
+  constexpr int kRows = kDzThreads / kDzSpan;  // rows at a time
+  __shared__ float sums[kRows][kDzSpan * W + 1];
+  const int col = threadIdx.x % kDzSpan, row = threadIdx.x / kDzSpan;
+  const int64_t j = (static_cast<int64_t>(blockIdx.x) * kDzSpan + col) * W;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per_block;
+  const int64_t r1 = r0 + rows_per_block < m ? r0 + rows_per_block : m;
+  float sum[W] = {};
+  bool bad = false;
+  if (j < n) {
+#pragma unroll 2
+    for (int64_t i = r0 + row; i < r1; i += kRows) {
+      float g[W];
+      if constexpr (W == 1)
+        g[0] = as_float(dy[i * ld_dy + j]);
+      else
+        load_row<W>(dy, kType, i * ld_dy + j, g);
+      if (act != OPR_ACT_NONE) {
+        float v[W];
+        if constexpr (W == 1)
+          v[0] = as_float(z[i * ldz + j]);
+        else
+          load_row<W>(z, kType, i * ldz + j, v);
+        // __fmul_rn: one value for the sum and for dz, whether or not dz is wanted
+        auto each = [&](auto slope) {
+#pragma unroll
+          for (int k = 0; k < W; ++k) g[k] = __fmul_rn(g[k], slope(v[k]));
+        };
+        if (act == OPR_ACT_SILU)
+          each([](float x) { return activate_slope(x, OPR_ACT_SILU); });
+        else if (act == OPR_ACT_GELU)
+          each([](float x) { return activate_slope(x, OPR_ACT_GELU); });
+        else
+          each([](float x) { return activate_slope(x, OPR_ACT_GELU_TANH); });
+      }
+#pragma unroll
+      for (int k = 0; k < W; ++k) sum[k] += g[k];
+      if (dz != nullptr) {
+        if constexpr (W == 1)
+          bad |= store_typed(dz, kType, i * ld_dz + j, g[0]);
+        else
+          bad |= store_row<W>(dz, kType, i * ld_dz + j, g);
+      }
+    }
+  }
+  if (bad && dev_status != nullptr) atomicOr(dev_status, OPR_DEV_FP16_RANGE);
+  if (partial == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < W; ++k) sums[row][col * W + k] = sum[k];
+  __syncthreads();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kDzSpan * W;
+  for (int c = threadIdx.x; c < kDzSpan * W && first + c < n; c += kDzThreads) {
+    float t = 0.f;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) t += sums[r][c];
+    partial[static_cast<int64_t>(blockIdx.y) * n + first + c] = t;
+  }
+}
+
+// Sums of the row blocks' partials, 32 columns a block, eight threads to a column,
+// added in a fixed order in fp64.
 __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, int32_t blocks, int32_t n, float* out) {
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (j >= n) return;
+  __shared__ double sums[8][33];
+  const int col = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + col;
   double t = 0.0;
-  for (int b = 0; b < blocks; ++b) t += partial[static_cast<int64_t>(b) * n + j];
+  if (j < n)
+#pragma unroll 4
+    for (int b = part; b < blocks; b += 8) t += partial[static_cast<int64_t>(b) * n + j];
+  sums[part][col] = t;
+  __syncthreads();
+  if (part != 0 || j >= n) return;
+  for (int p = 1; p < 8; ++p) t += sums[p][col];
   out[j] = static_cast<float>(t);
 }
 
@@ -747,6 +856,15 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // the clusters within its GPCs; as the occupancy query reports them).
 constexpr int kSlots[kMaxSplit] = {296, 296, 279, 284, 280, 270, 259, 264};
 
+// CTAs over which the depth of each tile is split: as many as run at one time, with
+// four slices or more to each.
+int tile_split(int64_t tiles, int64_t slices) {
+  int split = 1;
+  for (int c = 2; c <= kMaxSplit; ++c)
+    if (tiles * c <= kSlots[c - 1] && slices >= 4 * c) split = c;
+  return split;
+}
+
 template <bool P_MN, bool Q_MN, int BN, bool SWAP>
 cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
   CUtensorMap mp, mq;
@@ -759,10 +877,7 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cuda
   if (e != cudaSuccess) return e;
   const int64_t tiles_p = ceil_div(a.rows_p, kRowsP), tiles_q = ceil_div(a.rows_q, BN), tiles = tiles_p * tiles_q;
   const int64_t slices = ceil_div(a.depth, kDepth);
-  // the depth split over as many CTAs as run at one time, four slices or more to each
-  int split = 1;
-  for (int c = 2; c <= kMaxSplit; ++c)
-    if (tiles * c <= kSlots[c - 1] && slices >= 4 * c) split = c;
+  const int split = tile_split(tiles, slices);
   a.vec = vector_epilogue(a.e, SWAP ? a.rows_p : a.rows_q);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles_p * split), static_cast<unsigned>(tiles_q));
@@ -777,38 +892,43 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cuda
   return cudaLaunchKernelEx(&cfg, kernel, mp, mq, a);
 }
 
-template <bool P_MN, bool Q_MN, int BN>
+template <bool P_MN, bool Q_MN>
 cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
   CUtensorMap mp, mq;
   if (!operand_map(&mp, p, a.rows_p, a.depth, a.f16 != 0, kRowsP) ||
-      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, BN / 2))
+      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, kRowsP))
     return cudaErrorInvalidValue;
-  constexpr auto* kernel = product_pair_kernel<P_MN, Q_MN, BN>;
-  static_assert(sizeof(PairSmem<BN>) + 1024 <= kProductSmem, "the ring and the staging fit an SM");
+  constexpr auto* kernel = product_pair_kernel<P_MN, Q_MN>;
   const cudaError_t e = allow_smem<kernel>(kProductSmem);
   if (e != cudaSuccess) return e;
-  a.tiles_p = static_cast<int32_t>(ceil_div(a.rows_p, kPairRows));
-  a.tiles_q = static_cast<int32_t>(ceil_div(a.rows_q, BN));
+  a.tiles_p = static_cast<int32_t>(ceil_div(a.rows_p, kPairTile));
+  a.tiles_q = static_cast<int32_t>(ceil_div(a.rows_q, kPairTile));
   a.vec = vector_epilogue(a.e, a.rows_q);
   const int64_t pairs = std::min<int64_t>(static_cast<int64_t>(a.tiles_p) * a.tiles_q, 148 / 2);
   kernel<<<static_cast<unsigned>(2 * pairs), kProductThreads, kProductSmem, stream>>>(mp, mq, a);
   return cudaGetLastError();
 }
 
+// Which kernel: the least of the times (us) that the three shapes of work take, as
+// measured over products of 128 to 16384 rows, 144 to 4096 columns and 128 to 65536
+// deep (a few us of launch, pipeline fill and last epilogue, alike for all, left out):
+//   pairs     0.36 a 256 x 256 slice of 64, whole waves of 74 tiles
+//   tiles     0.27 a 128 x 128 slice or 0.20 a 128 x 64 slice per SM while two CTAs
+//             share it, but at least 0.36 or 0.25 a slice of one CTA's own chain
+// e.g. 777 x 4096 x 4096 (device us): pairs 32, tiles 35 and 47; 512 rows: 31, 24, 27;
+// 128 rows: 30, 17, 15; a weight gradient of 1024 x 1024 over 16384 rows: 88, 38, 48.
 template <bool P_MN, bool Q_MN>
 cudaError_t launch_product(const Operand& p, const Operand& q, const ProductArgs& a, cudaStream_t stream) {
-  auto pairs = [&](int bn) { return ceil_div(a.rows_p, kPairRows) * ceil_div(a.rows_q, bn); };
-  if (const char* f = getenv("LINF")) {
-    switch (atoi(f)) {
-      case 1: return launch_pairs<P_MN, Q_MN, 256>(p, q, a, stream);
-      case 2: return launch_pairs<P_MN, Q_MN, 128>(p, q, a, stream);
-      case 3: if constexpr (!Q_MN) return launch_pairs<P_MN, Q_MN, 64>(p, q, a, stream);
-      case 4: return launch_tiles<P_MN, Q_MN, 128, false>(p, q, a, stream);
-      case 5: return launch_tiles<P_MN, Q_MN, 64, false>(p, q, a, stream);
-    }
-  }
-  if (pairs(256) >= 74) return launch_pairs<P_MN, Q_MN, 256>(p, q, a, stream);
-  if (pairs(128) >= 48) return launch_pairs<P_MN, Q_MN, 128>(p, q, a, stream);
+  const double slices = static_cast<double>(ceil_div(a.depth, kDepth));
+  const double pairs = static_cast<double>(ceil_div(ceil_div(a.rows_p, kPairTile) * ceil_div(a.rows_q, 256), 74)) * slices * 0.36;
+  auto tiles = [&](int bn, double shared, double own) {
+    const int64_t n = ceil_div(a.rows_p, kRowsP) * ceil_div(a.rows_q, bn);
+    const int split = tile_split(n, ceil_div(a.depth, kDepth));
+    return std::max(n * slices / 148 * shared, static_cast<double>(ceil_div(n * split, 296)) * slices / split * own);
+  };
+  const double wide = tiles(128, 0.27, 0.36), narrow = tiles(64, 0.20, 0.25);
+  if (pairs <= wide && pairs <= narrow) return launch_pairs<P_MN, Q_MN>(p, q, a, stream);
+  if (wide <= narrow) return launch_tiles<P_MN, Q_MN, 128, false>(p, q, a, stream);
   return launch_tiles<P_MN, Q_MN, 64, false>(p, q, a, stream);
 }
 
@@ -846,40 +966,68 @@ cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t m, int32_t
   return b_mn ? launch_product<false, true>(a, b, args, stream) : launch_product<false, false>(a, b, args, stream);
 }
 
-cudaError_t launch_pack(const Operand& from, int64_t rows, int64_t cols, void* to, int64_t ld, cudaStream_t stream) {
+cudaError_t launch_pack(const PackJob (&jobs)[2], cudaStream_t stream) {
+  PackArgs a{};
+  for (int i = 0; i < 2; ++i) {
+    a.x[i] = static_cast<const uint16_t*>(jobs[i].from);
+    a.y[i] = static_cast<uint16_t*>(jobs[i].to);
+    a.ldx[i] = jobs[i].ld_from;
+    a.ldy[i] = jobs[i].ld_to;
+    a.rows[i] = jobs[i].from != nullptr ? jobs[i].rows : 0;
+    a.cols[i] = jobs[i].cols;
+  }
+  const int64_t rows = a.rows[0] + a.rows[1];
   if (rows == 0) return cudaSuccess;
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((rows * cols + 2047) / 2048, 148 * 16));
-  pack_kernel<<<blocks, 256, 0, stream>>>(static_cast<const uint16_t*>(from.p), from.row, rows, cols,
-                                          static_cast<uint16_t*>(to), ld);
+  pack_kernel<<<static_cast<unsigned>(std::min<int64_t>(ceil_div(rows, 8), 148 * 8)), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-int32_t linear_dz_blocks(int64_t m) {
-  return static_cast<int32_t>(std::min<int64_t>((m + kDzRows - 1) / kDzRows, 1024));
+namespace {
+struct DzPlan {
+  bool wide;  // eight columns a thread
+  int32_t cols, rows;  // blocks
+  int64_t rows_per_block;
+};
+DzPlan dz_plan(int64_t m, int32_t n, bool wide) {
+  DzPlan p{};
+  p.wide = wide;
+  p.cols = static_cast<int32_t>(ceil_div(n, kDzSpan * (wide ? 8 : 1)));
+  // row blocks: four blocks an SM in all, eight rows at least to each
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({ceil_div(148 * 4, p.cols), ceil_div(m, 8), kDzMaxBlocks}));
+  p.rows_per_block = ceil_div(m, want);
+  p.rows = m > 0 ? static_cast<int32_t>(ceil_div(m, p.rows_per_block)) : 0;
+  return p;
+}
+}  // namespace
+
+int32_t linear_dz_blocks(int64_t m, int32_t n) {
+  return std::max(dz_plan(m, n, true).rows, dz_plan(m, n, false).rows);
 }
 
 cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int64_t ldz, int32_t dtype, int64_t m,
                              int32_t n, int32_t activation, void* dz, int64_t ld_dz, float* db, float* partial,
                              int32_t* dev_status, cudaStream_t stream) {
-  const int32_t blocks = linear_dz_blocks(m);
-  const unsigned cols = static_cast<unsigned>((n + 255) / 256);
-  if (blocks > 0) {
-    const int64_t rows = (m + blocks - 1) / blocks;
-    const dim3 grid(cols, blocks);
+  auto fits = [](const void* p, int64_t ld) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0); };
+  const bool wide = n % 8 == 0 && fits(dy, ld_dy) && (activation == OPR_ACT_NONE || fits(z, ldz)) && fits(dz, ld_dz);
+  const DzPlan plan = dz_plan(m, n, wide);
+  if (plan.rows > 0) {
+    const dim3 grid(plan.cols, plan.rows);
     float* part = db != nullptr ? partial : nullptr;
-    if (dtype == OPR_DTYPE_BF16)
-      linear_dz_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(
-          static_cast<const __nv_bfloat16*>(dy), ld_dy, static_cast<const __nv_bfloat16*>(z), ldz, m, n, activation,
-          static_cast<__nv_bfloat16*>(dz), ld_dz, part, rows, dev_status);
-    else
-      linear_dz_kernel<__half><<<grid, 256, 0, stream>>>(static_cast<const __half*>(dy), ld_dy,
-                                                         static_cast<const __half*>(z), ldz, m, n, activation,
-                                                         static_cast<__half*>(dz), ld_dz, part, rows, dev_status);
-    const cudaError_t e = cudaGetLastError();
+    auto go = [&](auto type, auto width) {
+      using T = decltype(type);
+      linear_dz_kernel<T, decltype(width)::value><<<grid, kDzThreads, 0, stream>>>(
+          static_cast<const T*>(dy), ld_dy, static_cast<const T*>(z), ldz, m, n, activation, static_cast<T*>(dz), ld_dz,
+          part, plan.rows_per_block, dev_status);
+      return cudaGetLastError();
+    };
+    auto typed = [&](auto width) {
+      return dtype == OPR_DTYPE_BF16 ? go(__nv_bfloat16{}, width) : go(__half{}, width);
+    };
+    const cudaError_t e = wide ? typed(std::integral_constant<int, 8>{}) : typed(std::integral_constant<int, 1>{});
     if (e != cudaSuccess) return e;
   }
   if (db == nullptr) return cudaSuccess;
-  column_sum_kernel<<<cols, 256, 0, stream>>>(partial, blocks, n, db);
+  column_sum_kernel<<<static_cast<unsigned>(ceil_div(n, 32)), 256, 0, stream>>>(partial, plan.rows, n, db);
   return cudaGetLastError();
 }
 
