@@ -95,7 +95,7 @@ struct ProductArgs {
   int64_t depth;
   int32_t f16;
   int32_t tiles_p, tiles_q;  // product_pair_kernel
-  int32_t vec;  // y, z, residual and bias allow 16-byte accesses of eight neighbours
+  int32_t vec;  // the rows of y, z and the residual allow vector accesses
   LinearEpilogue e;
   int32_t* dev_status;
   uint32_t wait_ns;
@@ -425,13 +425,14 @@ __global__ void __launch_bounds__(kProductThreads, 2)
 // next one is multiplied.
 constexpr int kPairTile = 256;
 constexpr int kEpiWarps = 8;
-constexpr int kStageLd = 36;  // floats from row to row of a warp's 32 x 32 staging: 16-byte accesses without conflicts
+constexpr int kWarpStage = 4096;  // bytes a warp stages its outputs in: two 32 x 32 blocks of 16 bits, or one of 32
 
 struct PairSmem {
   static constexpr int kStageBytes = 2 * kRowsP * 128;
   static constexpr int kStages = 5;
   alignas(1024) uint8_t ring[kStages][kStageBytes];
-  alignas(16) float stage[kEpiWarps][32 * kStageLd];
+  alignas(1024) uint8_t stage[kEpiWarps][kWarpStage];
+  alignas(16) float bias[kEpiWarps][kRowsP];
   uint64_t full[kStages], empty[kStages];  // full: the leader's, counts both CTAs' bytes
   uint64_t acc_full[2], acc_empty[2];      // acc_empty: the leader's
   uint64_t done;
@@ -481,6 +482,98 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// Stores a 32 x 32 block staged by a warp (one lane calls), as one bulk group.
+__device__ __forceinline__ void store_block(const CUtensorMap* map, const uint8_t* from, int n, int m) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(from)), "r"(n), "r"(m)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until all but kLeft of this lane's groups have read their shared memory.
+template <int kLeft>
+__device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+
+// A lane's row of 32 values into a staged block, in the swizzle of the block's map:
+// 16 bits in 64-byte rows, 32 bits in 128-byte rows; without bank conflicts.
+__device__ __forceinline__ void stage_row16(uint8_t* block, int row, const float (&v)[32], bool f16, bool& bad) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float lo = v[8 * g + 2 * k], hi = v[8 * g + 2 * k + 1];
+      w[k] = f16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+    }
+    *reinterpret_cast<uint4*>(block + row * 64 + ((g ^ (row >> 1)) & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (f16) {
+    float top = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      top = fmaxf(top, fabsf(v[i]));
+      nan |= v[i] != v[i];
+    }
+    bad |= nan || top > 65504.f;
+  }
+}
+__device__ __forceinline__ void stage_row32(uint8_t* block, int row, const float (&v)[32]) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g)
+    *reinterpret_cast<float4*>(block + row * 128 + ((g ^ row) & 7) * 16) =
+        make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+}
+
+// A lane's row of a residual block, as loaded; columns past the end are not read.
+struct RawRow {
+  uint4 v[8];
+};
+__device__ __forceinline__ void fetch_residual(const LinearEpilogue& e, int64_t m, int64_t n0, int32_t cols, RawRow& raw) {
+  const bool wide = e.residual_dtype == OPR_DTYPE_FP32;
+  const int per = wide ? 4 : 8;  // entries of 16 bytes
+  const char* p = static_cast<const char*>(e.residual) + (m * e.ld_residual + n0) * (wide ? 4 : 2);
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    raw.v[g] = make_uint4(0, 0, 0, 0);
+    if (!wide && g >= 4) continue;
+    if (n0 + per * (g + 1) <= cols) {
+      raw.v[g] = reinterpret_cast<const uint4*>(p)[g];
+    } else if (n0 + per * g < cols) {  // the row's last entries
+      uint32_t w[4] = {0, 0, 0, 0};
+      for (int k = 0; k < per && n0 + per * g + k < cols; ++k) {
+        if (wide)
+          w[k] = reinterpret_cast<const uint32_t*>(p)[per * g + k];
+        else
+          w[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[per * g + k]) << (16 * (k & 1));
+      }
+      raw.v[g] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+__device__ __forceinline__ void add_residual(const RawRow& raw, int32_t dtype, float (&v)[32]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(raw.v);
+  if (dtype == OPR_DTYPE_FP32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(w[i]);
+  } else if (dtype == OPR_DTYPE_BF16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[2 * i] += __uint_as_float(w[i] << 16);
+      v[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] += f.x;
+      v[2 * i + 1] += f.y;
+    }
+  }
+}
+
 // Tile t of the walk: groups of kGroup tile rows, columns outer inside a group, so
 // that the pairs that run together share rows of P and Q in L2.
 constexpr int kGroup = 8;
@@ -495,6 +588,7 @@ __device__ __forceinline__ void tile_at(int t, int tiles_p, int tiles_q, int& tp
 template <bool P_MN, bool Q_MN>
 __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_z,
                         const __grid_constant__ ProductArgs a) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = PairSmem;
@@ -602,65 +696,117 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
       if (!warp_wait(&sm.done, 0, nullptr, kWaitLimitNs)) *abort_flag = 1;
     }
   } else {
+    // A warp finishes 32 rows (one a lane) x 128 columns of the CTA's tile in chunks of
+    // 32 columns: in registers, then staged and stored by TMA, which clips the ends.
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    float* stage = sm.stage[warp - 2];
+    uint8_t* stage = sm.stage[warp - 2];
+    float* bias = sm.bias[warp - 2];
     const LinearEpilogue& e = a.e;
-    const bool f16 = a.f16 != 0;
+    const bool f16 = a.f16 != 0, y32 = e.y_dtype == OPR_DTYPE_FP32, y16 = e.y_dtype == OPR_DTYPE_FP16;
     bool bad = false;
     int i = 0;
+    uint32_t turn = 0;  // blocks of 16 bits staged so far
+    // the block to stage next, free again (two take turns; a 32-bit one takes both)
+    auto block16 = [&]() {
+      if (lane == 0) {
+        if (y32)
+          stores_read<0>();
+        else
+          stores_read<1>();
+      }
+      __syncwarp();
+      return stage + (y32 ? 0 : (turn++ & 1) * (kWarpStage / 2));
+    };
+    auto send = [&](const CUtensorMap* map, const uint8_t* block, int64_t n, int64_t m) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) store_block(map, block, static_cast<int>(n), static_cast<int>(m));
+    };
     for (int t = first; t < tiles; t += pairs, ++i) {
       const int b = i & 1;
       int tp, tq;
       tile_at(t, a.tiles_p, a.tiles_q, tp, tq);
+      const int64_t m0 = static_cast<int64_t>(tp) * kPairTile + rank * kRowsP + quad * 32;
+      const int64_t nb = static_cast<int64_t>(tq) * kPairTile + half * kRowsP;
+      const int64_t m = m0 + lane;
+      const bool in_m = m0 < a.rows_p;
+      if (e.bias != nullptr) {
+        __syncwarp();
+        for (int k = lane; k < kRowsP; k += 32) bias[k] = nb + k < a.rows_q ? load_typed(e.bias, e.bias_dtype, nb + k) : 0.f;
+        __syncwarp();
+      }
+      // the residual comes one chunk ahead, the first while the products still run
+      RawRow raw;
+      const bool res = a.vec && e.residual != nullptr && m < a.rows_p;
+      if (res && nb < a.rows_q) fetch_residual(e, m, nb, a.rows_q, raw);
       if (!warp_wait(&sm.acc_full[b], (i >> 1) & 1, abort_flag, depth_limit(a.wait_ns, slices))) break;
       tc_fence_after();
-      const int64_t m0 = static_cast<int64_t>(tp) * kPairTile + rank * kRowsP + quad * 32;
-      // chunks of 32 columns; rolled loops, so that the eight warps run from the
-      // instruction cache (unrolled, fetching was the longest stall)
-      constexpr int kChunks = BN / 64;
-      const uint32_t acc = tl + b * BN + half * (BN / 2);
+      const uint32_t acc = tl + b * BN + half * kRowsP;
 #pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
-        const int64_t n0 = static_cast<int64_t>(tq) * BN + half * (BN / 2) + c * 32;
-        const bool inside = m0 < a.rows_p && n0 < a.rows_q;
-        const int64_t n = n0 + (lane & 3) * 8;
-        const bool mine = inside && a.vec && n < a.rows_q;
-        float bias[8];
-        if (mine) load_bias<8>(e, n, bias);
+      for (int c = 0; c < kRowsP / 32; ++c) {
+        const int64_t n0 = nb + 32 * c;
         uint32_t r[32];
         tmem_ld32(acc + 32 * c, r);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(stage + lane * kStageLd + 4 * q) =
-              make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
-        if (c + 1 == kChunks) {  // this warp has read its part of the accumulator
+        if (c + 1 == kRowsP / 32) {  // this warp has read its part of the accumulator
           tc_fence_before();
           if (lane == 0)
             asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                              peer_addr(smem_u32(&sm.acc_empty[b]), 0))
                          : "memory");
         }
-        __syncwarp();
-        if (mine) {
+        if (!in_m || n0 >= a.rows_q) continue;
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+        if (!a.vec) {  // rows of y, z or the residual off the 16-byte grid: a lane a column
+          __syncwarp();
+          stage_row32(stage, lane, v);
+          __syncwarp();
           const int rows = a.rows_p - m0 < 32 ? static_cast<int>(a.rows_p - m0) : 32;
+          if (n0 + lane < a.rows_q) {
 #pragma unroll 1
-          for (int row = lane >> 2; row < rows; row += 8) {
-            float residual[8];
-            load_residual<8>(e, m0 + row, n, residual);
-            const float4* f = reinterpret_cast<const float4*>(stage + row * kStageLd + (lane & 3) * 8);
-            const float4 x = f[0], y = f[1];
-            float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            bad |= finish_row<8>(e, f16, m0 + row, n, v, bias, residual);
+            for (int row = 0; row < rows; ++row) {
+              const uint8_t* at = stage + row * 128 + (((lane >> 2) ^ row) & 7) * 16 + (lane & 3) * 4;
+              bad |= finish(e, f16, m0 + row, n0 + lane, *reinterpret_cast<const float*>(at));
+            }
           }
-        } else if (inside && !a.vec && n0 + lane < a.rows_q) {
-#pragma unroll 1
-          for (int row = 0; row < 32 && m0 + row < a.rows_p; ++row)
-            bad |= finish(e, f16, m0 + row, n0 + lane, stage[row * kStageLd + lane]);
+          continue;
         }
-        __syncwarp();
+        if (e.bias != nullptr) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float4 x = reinterpret_cast<const float4*>(bias + 32 * c)[g];
+            v[4 * g] += x.x;
+            v[4 * g + 1] += x.y;
+            v[4 * g + 2] += x.z;
+            v[4 * g + 3] += x.w;
+          }
+        }
+        if (e.z != nullptr) {
+          uint8_t* block = block16();
+          bool over = false;
+          stage_row16(block, lane, v, f16, over);
+          bad |= over && m < a.rows_p;
+          send(&map_z, block, n0, m0);
+        }
+        activate_row<32>(v, e.activation);
+        if (res) {
+          add_residual(raw, e.residual_dtype, v);
+          if (c + 1 < kRowsP / 32 && n0 + 32 < a.rows_q) fetch_residual(e, m, n0 + 32, a.rows_q, raw);
+        }
+        uint8_t* block = block16();
+        if (y32) {
+          stage_row32(block, lane, v);
+        } else {
+          bool over = false;
+          stage_row16(block, lane, v, y16, over);
+          bad |= over && m < a.rows_p;
+        }
+        send(&map_y, block, n0, m0);
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (bad) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
   }
   __syncthreads();
@@ -829,6 +975,19 @@ bool operand_map(CUtensorMap* map, const Operand& o, int64_t rows, int64_t depth
                       const_cast<void*>(o.p), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// An output matrix as a map of the 32 x 32 blocks that a warp stages.
+bool block_map(CUtensorMap* map, void* p, int64_t ld, int32_t dtype, int64_t rows, int64_t cols) {
+  const bool wide = dtype == OPR_DTYPE_FP32;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * (wide ? 4 : 2)};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode_tiled(map, wide                       ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                           : dtype == OPR_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      2, p, dims, strides, box, estr, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 // Lets a kernel use `bytes` of shared memory, once per device and kernel.
 template <auto* kKernel>
 cudaError_t allow_smem(int bytes) {
@@ -843,11 +1002,12 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-bool vector_epilogue(const LinearEpilogue& e, int64_t n) {
+// Do all rows of y, z and the residual start on 16-byte boundaries?
+bool rows_aligned(const LinearEpilogue& e) {
   auto fits = [](const void* p, int64_t ld) {
     return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0);
   };
-  return n % 8 == 0 && fits(e.y, e.ldy) && fits(e.z, e.ldz) && fits(e.residual, e.ld_residual) && fits(e.bias, 0);
+  return fits(e.y, e.ldy) && fits(e.z, e.ldz) && fits(e.residual, e.ld_residual);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -878,7 +1038,7 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cuda
   const int64_t tiles_p = ceil_div(a.rows_p, kRowsP), tiles_q = ceil_div(a.rows_q, BN), tiles = tiles_p * tiles_q;
   const int64_t slices = ceil_div(a.depth, kDepth);
   const int split = tile_split(tiles, slices);
-  a.vec = vector_epilogue(a.e, SWAP ? a.rows_p : a.rows_q);
+  a.vec = rows_aligned(a.e) && (SWAP ? a.rows_p : a.rows_q) % 4 == 0 && reinterpret_cast<uintptr_t>(a.e.bias) % 16 == 0;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles_p * split), static_cast<unsigned>(tiles_q));
   cfg.blockDim = dim3(kProductThreads);
@@ -903,9 +1063,13 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cuda
   if (e != cudaSuccess) return e;
   a.tiles_p = static_cast<int32_t>(ceil_div(a.rows_p, kPairTile));
   a.tiles_q = static_cast<int32_t>(ceil_div(a.rows_q, kPairTile));
-  a.vec = vector_epilogue(a.e, a.rows_q);
+  a.vec = rows_aligned(a.e);
+  CUtensorMap my = mp, mz = mp;  // not used where the epilogue is entry by entry, or without z
+  if (a.vec && (!block_map(&my, a.e.y, a.e.ldy, a.e.y_dtype, a.rows_p, a.rows_q) ||
+                (a.e.z != nullptr && !block_map(&mz, a.e.z, a.e.ldz, a.f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, a.rows_p, a.rows_q))))
+    return cudaErrorInvalidValue;
   const int64_t pairs = std::min<int64_t>(static_cast<int64_t>(a.tiles_p) * a.tiles_q, 148 / 2);
-  kernel<<<static_cast<unsigned>(2 * pairs), kProductThreads, kProductSmem, stream>>>(mp, mq, a);
+  kernel<<<static_cast<unsigned>(2 * pairs), kProductThreads, kProductSmem, stream>>>(mp, mq, my, mz, a);
   return cudaGetLastError();
 }
 

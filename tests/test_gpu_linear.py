@@ -240,7 +240,8 @@ def test_linear_on_a_side_stream_and_in_a_graph(sizes):
     assert all(torch.equal(a, b) for a, b in zip(other, held))
 
 
-@pytest.mark.parametrize("sizes", [(257, 264, 128), (2300, 2304, 200), (2200, 2056, 72), (6000, 1001, 136)], ids=str)
+@pytest.mark.parametrize("sizes", [(257, 264, 128), (2300, 2304, 200), (2200, 2056, 72), (6000, 1001, 136),
+                                   (2600, 2068, 64), (4100, 1500, 640)], ids=str)
 def test_large_products_match_oracle(sizes):
     """Enough 256 x 256 tiles for every pair of SMs to take more than one, with ends inside tiles in each
     direction."""
@@ -260,6 +261,29 @@ def test_large_products_match_oracle(sizes):
     # the transposed problem has the same dw, transposed: other operands, other tiles
     _, dwt, _ = opr.opr_linear_bwd(x, dy, torch.zeros(k, n, dtype=torch.bfloat16, device="cuda"), need_dx=False)
     within(dwt, to64(x).T @ to64(dy), sum_bound(to64(x).T, to64(dy).T, m), "bf16")
+
+
+@pytest.mark.parametrize("activation", [None, "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("types", [("bf16", "bf16", "bf16", "bf16"), ("fp16", "fp32", "bf16", "fp16"),
+                                   ("bf16", "fp16", "fp32", "fp32"), ("fp16", None, "fp16", "bf16"),
+                                   ("bf16", "bf16", None, "fp16")])
+def test_large_epilogues(types, activation):
+    """As test_linear_epilogues with z kept, where the products go through the CTA pairs; n ends inside a
+    block of 32 columns, and inside eight entries of it."""
+    dtype, bt, rt, yt = types
+    rng = np.random.default_rng(13)
+    for m, n, k in ((2500, 2076, 64), (2311, 2304, 72)):
+        x, w = matrix(rng, m, k, dtype), matrix(rng, n, k, dtype, scale=2 * k ** -0.5)
+        b = matrix(rng, 1, n, bt)[0] if bt else None
+        ld = (n + 7) // 8 * 8
+        r = matrix(rng, m, n, rt, wide=ld - n) if rt else None
+        out = torch.full((m, ld), 5.0, dtype=TYPES[yt], device="cuda")
+        y, z = opr.opr_linear(x, w, b, activation, r, out=out[:, :n], save_z=True)
+        assert (out[:, n:] == 5).all()
+        ry, rz = lo.linear(to64(x), to64(w), 0 if b is None else to64(b), activation, None if r is None else to64(r))
+        bz = sum_bound(to64(x), to64(w), k) + (np.abs(rz) + 2) * 2.0 ** -23
+        within(z, rz, bz, dtype, f"z {m, n, k}")
+        within(y, ry, act_bound(rz, bz, activation) + (np.abs(ry) + 4) * 2.0 ** -23, yt, f"{m, n, k}")
 
 
 @pytest.mark.parametrize("sizes", [(3, 64, 4096), (300, 300, 4096), (6000, 1024, 512)], ids=str)
