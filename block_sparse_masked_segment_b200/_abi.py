@@ -669,6 +669,16 @@ def _call(name: str, device: torch.device, *args) -> None:
         _check(st, name)
 
 
+def _new(shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """An empty contiguous tensor (empty_strided takes half of torch.empty's time, and a call here
+    allocates up to six)."""
+    strides, step = [], 1
+    for n in reversed(shape):
+        strides.append(step)
+        step *= n
+    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
+
+
 def _one_device(call: str, first: torch.Tensor, *ts: torch.Tensor | None) -> None:
     device = first.device
     for t in ts:
@@ -746,12 +756,13 @@ def opr_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k
     if out is None:
         if out_dtype not in _DT:
             raise OprError("out_dtype must be bf16, fp16 or fp32")
-        out = tuple(torch.empty(t.shape, dtype=out_dtype, device=q.device) for t in ins)
-    if len(out) != len(ins):
-        raise OprError("out must be (q_out, k_out), with v (q_out, k_out, v_out)")
-    _need_cuda(*out)
-    if any(o.shape != t.shape or o.dtype not in _DT or o.dtype != out[0].dtype for o, t in zip(out, ins)):
-        raise OprError("out must have the shapes of q, k and v and one type of bf16, fp16 or fp32")
+        out = tuple([_new(t.shape, out_dtype, q.device) for t in ins])
+    else:
+        if len(out) != len(ins):
+            raise OprError("out must be (q_out, k_out), with v (q_out, k_out, v_out)")
+        _need_cuda(*out)
+        if any(o.shape != t.shape or o.dtype not in _DT or o.dtype != out[0].dtype for o, t in zip(out, ins)):
+            raise OprError("out must have the shapes of q, k and v and one type of bf16, fp16 or fp32")
     _one_device("opr_qk_norm_rope", q, k, v, q_weight, k_weight, *out)
     _call("opr_qk_norm_rope", q.device, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _DT[q.dtype], _ptr(q_weight),
           _ptr(k_weight), _DT[q_weight.dtype], eps, _ptr(pos_id), _ptr(freq), 2 * freq.numel(), bool(interleaved), scale,
@@ -783,25 +794,26 @@ def opr_qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k:
     grads = (dq, dk) if dv is None else (dq, dk, dv)
     shapes = (q.shape, k.shape, k.shape)
     _need_cuda(*grads)
-    if any(g.shape != sh or g.dtype not in _DT or g.dtype != dq.dtype for g, sh in zip(grads, shapes)):
+    if dq.dtype not in _DT or any([g.shape != sh or g.dtype != dq.dtype for g, sh in zip(grads, shapes)]):
         raise OprError("dq, dk and dv must have the shapes of q, k and v and one type of bf16, fp16 or fp32")
     if out is None:
         out_dtype = q.dtype if out_dtype is None else out_dtype
         if out_dtype not in _DT:
             raise OprError("out_dtype must be bf16, fp16 or fp32")
-        out = tuple(torch.empty(g.shape, dtype=out_dtype, device=q.device) for g in grads)
-    if len(out) != len(grads):
-        raise OprError("out must be (dq_in, dk_in), with dv (dq_in, dk_in, dv_in)")
-    strides = [_heads("out", o, total, d, g.shape[1]) for o, g in zip(out, grads)]
-    if any(o.dtype != out[0].dtype for o in out):
-        raise OprError("the tensors of out must have one type")
-    _one_device("opr_qk_norm_rope_bwd", q, k, q_weight, k_weight, *grads, *out)
-    wb = max(opr_qk_norm_rope_bwd_workspace_bytes(total, hq, hkv, d), 256)
+        out = tuple([_new(g.shape, out_dtype, q.device) for g in grads])
+        strides = (hq * d, hkv * d, hkv * d)
+    else:
+        if len(out) != len(grads):
+            raise OprError("out must be (dq_in, dk_in), with dv (dq_in, dk_in, dv_in)")
+        strides = [_heads("out", o, total, d, g.shape[1]) for o, g in zip(out, grads)]
+        if any(o.dtype != out[0].dtype for o in out):
+            raise OprError("the tensors of out must have one type")
     if workspace is None:
-        workspace = torch.empty(wb, dtype=torch.uint8, device=q.device)
-    _need_cuda(workspace)
-    _one_device("opr_qk_norm_rope_bwd", q, workspace)
-    dqw, dkw = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in range(2))
+        workspace = _new((opr_qk_norm_rope_bwd_workspace_bytes(total, hq, hkv, d),), torch.uint8, q.device)
+    else:
+        _need_cuda(workspace)
+    _one_device("opr_qk_norm_rope_bwd", q, k, q_weight, k_weight, workspace, *grads, *out)
+    dqw, dkw = _new((d,), torch.float32, q.device), _new((d,), torch.float32, q.device)
     _call("opr_qk_norm_rope_bwd", q.device, _ptr(dq), _ptr(dk), _ptr(dv), _DT[dq.dtype], _ptr(q), qs, _ptr(k), ks,
           _DT[q.dtype], _ptr(q_weight), _ptr(k_weight), _DT[q_weight.dtype], eps, _ptr(pos_id), _ptr(freq),
           2 * freq.numel(), bool(interleaved), scale, _ptr(row_map), total, hq, hkv, d, _ptr(out[0]), strides[0],
@@ -840,7 +852,7 @@ def _status_word(dev_status, device) -> torch.Tensor:
 def _scratch(workspace, need: int, device):
     """The caller's workspace, or one of `need` bytes (None for 0): (tensor, bytes)."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        workspace = _new((need,), torch.uint8, device) if need else None
     elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
         raise OprError(f"workspace must be contiguous on {device}")
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -883,9 +895,9 @@ def opr_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
         out_dtype = x.dtype if out_dtype is None else out_dtype
         if out_dtype not in _DT:
             raise OprError("out_dtype must be bf16, fp16 or fp32")
-        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
+        out = _new((m, n), out_dtype, x.device)
     ldy = _matrix("out", out, shape=(m, n))
-    z = torch.empty((m, n), dtype=x.dtype, device=x.device) if save_z else None
+    z = _new((m, n), x.dtype, x.device) if save_z else None
     _one_device("opr_linear", x, w, bias, residual, out)
     status = _status_word(dev_status, x.device)
     need = load_library().opr_linear_workspace_bytes(_ptr(x), ldx, _ptr(w), ldw, m, n, k)
@@ -942,11 +954,11 @@ def opr_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.
             return given
         if dtype not in _DT:
             raise OprError("gradients are bf16, fp16 or fp32")
-        return torch.empty(shape, dtype=dtype, device=x.device)
+        return _new(shape, dtype, x.device)
 
     dx = result(out[0], need_dx, x.dtype if dx_dtype is None else dx_dtype, (m, k))
     dw = result(out[1], need_dw, w.dtype if dw_dtype is None else dw_dtype, (n, k))
-    db = torch.empty(n, dtype=torch.float32, device=x.device) if bias else None
+    db = _new((n,), torch.float32, x.device) if bias else None
     ldx_out = 0 if dx is None else _matrix("dx", dx, shape=(m, k))
     ldw_out = 0 if dw is None else _matrix("dw", dw, shape=(n, k))
     _one_device("opr_linear_bwd", x, w, dy, z, dx_residual, dx, dw)

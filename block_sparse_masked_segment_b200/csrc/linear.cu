@@ -13,15 +13,36 @@
 namespace opr {
 namespace {
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// The activations bound the epilogues of short products, so they take the fast
+// exponential and quotient (a few steps of the last place; 0 and 1 at the ends).
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 // gelu with tanh: z/2 (1 + tanh u) = z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3)
 constexpr float kGeluC = 0.79788456080286536f, kGeluA = 0.044715f, kSqrtHalf = 0.70710678118654752f,
                 kInvSqrt2Pi = 0.39894228040143268f;
 
+// Phi(z), the normal distribution function, and e = exp(-z^2 / 2): with x = |z| / sqrt 2,
+// 1 - erf(x) = (a1 t + ... + a5 t^5) e, t = 1 / (1 + p x) (Abramowitz and Stegun 7.1.26,
+// within 1.5e-7).  With erff the products with this activation took up to 1.2 times as
+// long (dz of 2377 x 4096: 22 against 18 us).
+__device__ __forceinline__ float normal(float z, float& e) {
+  const float x = fabsf(z) * kSqrtHalf;
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  e = __expf(-x * x);
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  const float tail = 0.5f * p * t * e;  // of the side beyond |z|
+  return z < 0.f ? tail : 1.f - tail;
+}
+
 __device__ __forceinline__ float activate(float z, int32_t act) {
   if (act == OPR_ACT_SILU) return z * sigmoid(z);
-  if (act == OPR_ACT_GELU) return 0.5f * z * (1.f + erff(z * kSqrtHalf));
+  if (act == OPR_ACT_GELU) {
+    float e;
+    return z * normal(z, e);
+  }
   if (act == OPR_ACT_GELU_TANH) return z * sigmoid(2.f * kGeluC * (z + kGeluA * z * z * z));
   return z;
 }
@@ -31,7 +52,11 @@ __device__ __forceinline__ float activate_slope(float z, int32_t act) {
     const float s = sigmoid(z);
     return s * (1.f + z * (1.f - s));
   }
-  if (act == OPR_ACT_GELU) return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+  if (act == OPR_ACT_GELU) {
+    float e;
+    const float phi = normal(z, e);
+    return phi + z * kInvSqrt2Pi * e;
+  }
   if (act == OPR_ACT_GELU_TANH) {
     const float s = sigmoid(2.f * kGeluC * (z + kGeluA * z * z * z));
     return s * (1.f + 2.f * z * (1.f - s) * kGeluC * (1.f + 3.f * kGeluA * z * z));
@@ -62,20 +87,45 @@ constexpr int kRowsP = 128;
 constexpr int kDepth = 64;
 constexpr int kChunk = kDepth * 128;  // bytes of an MN-major chunk
 
-template <bool MN>
-__device__ __forceinline__ void load_slice(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int row0, int k0,
-                                           int rows) {
+// Loads a 64-deep slice of `rows` rows from row0 into dst; PAIR: for a CTA pair, `bar`
+// (a shared::cluster address) may be the peer's.  A K-major slice is one box.  An
+// MN-major one is a box of all its chunks where the map is of chunks (`folded`, rows a
+// multiple of 64), else a box a chunk: every box more in a slice costs the copy engine
+// time (a pair's products with four boxes a slice took 1.09 times as long as with two).
+template <bool MN, bool PAIR>
+__device__ __forceinline__ void load_slice(const CUtensorMap* map, uint32_t bar, uint8_t* dst, int row0, int k0, int rows,
+                                           bool folded) {
   auto box = [&](uint8_t* to, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            smem_u32(to)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
-        : "memory");
+    if constexpr (PAIR)
+      asm volatile(
+          "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+          " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(to)),
+          "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+          : "memory");
+    else
+      asm volatile(
+          "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+          " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(to)),
+          "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+          : "memory");
   };
-  if constexpr (MN) {
-    for (int c = 0; c < rows / 64; ++c) box(dst + c * kChunk, row0 + 64 * c, k0);
-  } else {
+  if constexpr (!MN) {
     box(dst, k0, row0);
+  } else if (folded) {
+    if constexpr (PAIR)
+      asm volatile(
+          "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+          " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+          "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(k0), "r"(row0 / 64)
+          : "memory");
+    else
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+          " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+          "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(k0), "r"(row0 / 64)
+          : "memory");
+  } else {
+    for (int c = 0; c < rows / 64; ++c) box(dst + c * kChunk, row0 + 64 * c, k0);
   }
 }
 
@@ -94,7 +144,8 @@ struct ProductArgs {
   int32_t rows_q;
   int64_t depth;
   int32_t f16;
-  int32_t tiles_p, tiles_q;  // product_pair_kernel
+  int32_t folded_p, folded_q;  // MN-major operands: the map is of chunks (load_slice)
+  int32_t tiles_p, tiles_q;    // product_pair_kernel
   int32_t vec;  // the rows of y, z and the residual allow vector accesses
   LinearEpilogue e;
   int32_t* dev_status;
@@ -314,8 +365,10 @@ __global__ void __launch_bounds__(kProductThreads, 2)
         const int s = j % kStages;
         if (j >= kStages && !mbar_wait(&sm.empty[s], ((j / kStages) + 1) & 1, abort_flag, a.wait_ns)) break;
         mbar_arrive_expect_tx(&sm.full[s], kBytes);
-        load_slice<P_MN>(&map_p, &sm.full[s], sm.ring[s], static_cast<int>(p0), (s0 + j) * kDepth, kRowsP);
-        load_slice<Q_MN>(&map_q, &sm.full[s], sm.ring[s] + kRowsP * 128, q0, (s0 + j) * kDepth, kRowsQ);
+        load_slice<P_MN, false>(&map_p, smem_u32(&sm.full[s]), sm.ring[s], static_cast<int>(p0), (s0 + j) * kDepth, kRowsP,
+                                a.folded_p != 0);
+        load_slice<Q_MN, false>(&map_q, smem_u32(&sm.full[s]), sm.ring[s] + kRowsP * 128, q0, (s0 + j) * kDepth, kRowsQ,
+                                a.folded_q != 0);
         issued = j + 1;
       }
       // every copy issued has landed before the CTA goes on (also after an abort)
@@ -441,24 +494,6 @@ struct PairSmem {
   int issued;
 };
 static_assert(sizeof(PairSmem) + 1024 <= kProductSmem, "the ring and the staging fit an SM");
-
-// Loads 128 rows of an operand for the pair; `bar` is the leader's barrier (cluster address).
-template <bool MN>
-__device__ __forceinline__ void load_pair_slice(const CUtensorMap* map, uint32_t bar, uint8_t* dst, int row0, int k0) {
-  auto box = [&](uint8_t* to, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(to)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
-        : "memory");
-  };
-  if constexpr (MN) {
-#pragma unroll
-    for (int c = 0; c < kRowsP / 64; ++c) box(dst + c * kChunk, row0 + 64 * c, k0);
-  } else {
-    box(dst, k0, row0);
-  }
-}
 
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
@@ -634,9 +669,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     // the leader's barrier counts both CTAs' bytes of the stage
     if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Smem::kStageBytes);
     const uint32_t bar = peer_addr(smem_u32(&sm.full[s]), 0);
-    load_pair_slice<P_MN>(&map_p, bar, sm.ring[s], tp * kPairTile + static_cast<int>(rank) * kRowsP, slice * kDepth);
-    load_pair_slice<Q_MN>(&map_q, bar, sm.ring[s] + kRowsP * 128, tq * kPairTile + static_cast<int>(rank) * kRowsP,
-                          slice * kDepth);
+    load_slice<P_MN, true>(&map_p, bar, sm.ring[s], tp * kPairTile + static_cast<int>(rank) * kRowsP, slice * kDepth, kRowsP,
+                           a.folded_p != 0);
+    load_slice<Q_MN, true>(&map_q, bar, sm.ring[s] + kRowsP * 128, tq * kPairTile + static_cast<int>(rank) * kRowsP,
+                           slice * kDepth, kRowsP, a.folded_q != 0);
   };
 
   if (warp == 0) {
@@ -963,16 +999,24 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, i
 
 namespace {
 
-// A 16-bit operand as a 2-D map of boxes of `box_rows` rows of 64 entries along its
-// contiguous direction, 128-byte swizzle.
-bool operand_map(CUtensorMap* map, const Operand& o, int64_t rows, int64_t depth, bool f16, int box_rows) {
+// A 16-bit operand as a map of slices of `box_rows` rows, 64 deep, 128-byte swizzle:
+// of rows and depth, or folded (set to 1) of an MN-major operand's chunks of 64 rows.
+bool operand_map(CUtensorMap* map, const Operand& o, int64_t rows, int64_t depth, bool f16, int box_rows,
+                 int32_t* folded) {
   const bool mn = o.col != 1;
+  const auto type = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t pitch = static_cast<cuuint64_t>(mn ? o.col : o.row) * 2;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  *folded = mn && rows % 64 == 0;
+  if (*folded) {
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(depth), static_cast<cuuint64_t>(rows / 64)};
+    const cuuint64_t strides[2] = {pitch, 128};
+    const cuuint32_t box[3] = {64, kDepth, static_cast<cuuint32_t>(box_rows / 64)};
+    return encode_tiled(map, type, 3, const_cast<void*>(o.p), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
+  }
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(mn ? rows : depth), static_cast<cuuint64_t>(mn ? depth : rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(mn ? o.col : o.row) * 2};
   const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(mn ? kDepth : box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode_tiled(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                      const_cast<void*>(o.p), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_tiled(map, type, 2, const_cast<void*>(o.p), dims, &pitch, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // An output matrix as a map of the 32 x 32 blocks that a warp stages.
@@ -1028,8 +1072,8 @@ int tile_split(int64_t tiles, int64_t slices) {
 template <bool P_MN, bool Q_MN, int BN, bool SWAP>
 cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
   CUtensorMap mp, mq;
-  if (!operand_map(&mp, p, a.rows_p, a.depth, a.f16 != 0, kRowsP) ||
-      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, BN))
+  if (!operand_map(&mp, p, a.rows_p, a.depth, a.f16 != 0, kRowsP, &a.folded_p) ||
+      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, TileSmem<Q_MN, BN>::kRowsQ, &a.folded_q))
     return cudaErrorInvalidValue;
   constexpr auto* kernel = product_tile_kernel<P_MN, Q_MN, BN, SWAP>;
   static_assert(sizeof(TileSmem<Q_MN, BN>) + 1024 <= kTileSmem, "a tile's ring fits half an SM");
@@ -1055,8 +1099,8 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cuda
 template <bool P_MN, bool Q_MN>
 cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cudaStream_t stream) {
   CUtensorMap mp, mq;
-  if (!operand_map(&mp, p, a.rows_p, a.depth, a.f16 != 0, kRowsP) ||
-      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, kRowsP))
+  if (!operand_map(&mp, p, a.rows_p, a.depth, a.f16 != 0, kRowsP, &a.folded_p) ||
+      !operand_map(&mq, q, a.rows_q, a.depth, a.f16 != 0, kRowsP, &a.folded_q))
     return cudaErrorInvalidValue;
   constexpr auto* kernel = product_pair_kernel<P_MN, Q_MN>;
   const cudaError_t e = allow_smem<kernel>(kProductSmem);

@@ -71,6 +71,35 @@ def test_linear_epilogues(types, activation):
         within(y, ry, act_bound(rz, bz, activation) + (np.abs(ry) + 4) * 2.0 ** -23, yt, f"{m, n, k}")
 
 
+@pytest.mark.parametrize("activation", ["silu", "gelu", "gelu_tanh"])
+def test_activations_over_their_whole_range(activation):
+    """Every exponent of z, both signs, the ends and NaN, through a product by one: forward within 2^-20 of
+    |z| + 1, slope (the gradient of y for dy = 1) within 2^-19; far out they are 0 or z, 0 or 1."""
+    e = np.arange(-40, 41)
+    z = np.concatenate([s * m * 2.0 ** e for s in (1, -1) for m in (1, 1.25, 1.5, 1.75)] + [[0.0], np.linspace(-9, 9, 511)])
+    z = torch.from_numpy(z.astype(np.float32)).to("cuda", torch.bfloat16)
+    one = torch.zeros(8, 8, dtype=torch.bfloat16, device="cuda")
+    one[0, 0] = 1
+    x = torch.zeros(len(z), 8, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = z
+    y = opr.opr_linear(x, one, activation=activation, out_dtype=torch.float32)[:, 0]
+    Z = to64(z)
+    with np.errstate(over="ignore"):
+        ref, slope = lo.act(Z, activation), lo.act_slope(Z, activation)
+    big = np.abs(Z) > 1e6  # z^3 overflows in the plain formula: the limits
+    ref[big], slope[big] = np.where(Z[big] > 0, Z[big], 0), np.where(Z[big] > 0, 1, 0)
+    within(y, ref, (np.abs(Z) + 1) * 2.0 ** -20 * np.where(np.abs(Z) > 64, 0.25, 1), "fp32")
+    dy = torch.ones(len(z), 1, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(1, 8, dtype=torch.bfloat16, device="cuda")
+    dz, _, _ = opr.opr_linear_bwd(dy, x, w, z[:, None], activation, need_dw=False, dx_dtype=torch.float32)
+    within(dz[:, 0], slope, 2.0 ** -19 + half_step("bf16") * np.abs(slope), "fp32")
+    for v in (float("nan"), float("inf"), float("-inf")):
+        x[0, 0] = v
+        got = opr.opr_linear(x, one, activation=activation, out_dtype=torch.float32)[0, 0]
+        want = torch.nn.functional.silu(torch.tensor(v)) if v != float("inf") else torch.tensor(v)
+        assert torch.isnan(got) == torch.isnan(want) and (v != float("inf") or got == v)
+
+
 @pytest.mark.parametrize("wide,offset", [(8, 0), (8, 8), (64, 16), (3, 0), (8, 1)])
 def test_linear_on_parts_of_wider_rows(wide, offset):
     """Operands, residual and result inside wider rows, on and off the 16-byte grid; nothing else is written,
