@@ -262,6 +262,52 @@ __device__ __forceinline__ void load_residual(const LinearEpilogue& e, int64_t m
   if (e.residual != nullptr) load_row<W>(e.residual, e.residual_dtype, m * e.ld_residual + n, v);
 }
 
+// Four entries of row m, 32 apart (neighbouring lanes take neighbouring ones), those of
+// `in` only: any alignment.  The loads go out together.
+__device__ __forceinline__ void load_apart(const void* p, int32_t dtype, int64_t i, const bool (&in)[4], float (&v)[4]) {
+  auto each = [&](auto type) {
+    using T = decltype(type);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = in[k] ? as_float(static_cast<const T*>(p)[i + 32 * k]) : 0.f;
+  };
+  if (dtype == OPR_DTYPE_BF16)
+    each(__nv_bfloat16{});
+  else if (dtype == OPR_DTYPE_FP16)
+    each(__half{});
+  else
+    each(float{});
+}
+__device__ __forceinline__ bool store_apart(void* p, int32_t dtype, int64_t i, const bool (&in)[4], const float (&v)[4]) {
+  bool bad = false;
+  auto each = [&](auto type) {
+    using T = decltype(type);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (in[k]) {
+        bad |= beyond<T>(v[k]);
+        static_cast<T*>(p)[i + 32 * k] = from_float<T>(v[k]);
+      }
+  };
+  if (dtype == OPR_DTYPE_BF16)
+    each(__nv_bfloat16{});
+  else if (dtype == OPR_DTYPE_FP16)
+    each(__half{});
+  else
+    each(float{});
+  return bad;
+}
+__device__ __forceinline__ bool finish_apart(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, const bool (&in)[4],
+                                             float (&v)[4], const float (&bias)[4], const float (&residual)[4]) {
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] += bias[k];
+  if (e.z != nullptr) bad |= store_apart(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, in, v);
+  activate_row<4>(v, e.activation);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] += residual[k];
+  return store_apart(e.y, e.y_dtype, m * e.ldy + n, in, v) || bad;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -279,6 +325,11 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
+}
+__device__ __forceinline__ float load_peer(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ float4 load_peer4(uint32_t addr) {
   float4 v;
@@ -428,39 +479,54 @@ __global__ void __launch_bounds__(kProductThreads, 2)
 #pragma unroll
   for (int r = 0; r < kMaxSplit; ++r) peer[r] = peer_addr(base, r < static_cast<int>(ranks) ? r : 0);
   bool bad = false;
-  constexpr int kQuads = kLine / 4;  // groups of four entries of a line
-  for (int i = threadIdx.x + static_cast<int>(rank) * kProductThreads; i < lines * kQuads;
-       i += static_cast<int>(ranks) * kProductThreads) {
-    const int line = i / kQuads, j = i % kQuads * 4;
-    if (j >= len) continue;
-    const uint32_t at = 4 * (line * kLineLd + j);
-    float bias[4], residual[4];
-    if (a.vec) {
+  if (a.vec) {
+    constexpr int kQuads = kLine / 4;  // groups of four neighbours of a line
+    for (int i = threadIdx.x + static_cast<int>(rank) * kProductThreads; i < lines * kQuads;
+         i += static_cast<int>(ranks) * kProductThreads) {
+      const int line = i / kQuads, j = i % kQuads * 4;
+      if (j >= len) continue;
+      float bias[4], residual[4];
       load_bias<4>(a.e, n0 + j, bias);
       load_residual<4>(a.e, m0 + line, n0 + j, residual);
-    }
-    float4 v;
-    if (ranks == 1) {
-      v = *reinterpret_cast<const float4*>(part + line * kLineLd + j);
-    } else {
-      v = load_peer4(peer[0] + at);
+      const uint32_t at = 4 * (line * kLineLd + j);
+      float4 v;
+      if (ranks == 1) {
+        v = *reinterpret_cast<const float4*>(part + line * kLineLd + j);
+      } else {
+        v = load_peer4(peer[0] + at);
 #pragma unroll
-      for (int r = 1; r < kMaxSplit; ++r) {
-        if (r >= static_cast<int>(ranks)) break;
-        const float4 x = load_peer4(peer[r] + at);
-        v.x += x.x;
-        v.y += x.y;
-        v.z += x.z;
-        v.w += x.w;
+        for (int r = 1; r < kMaxSplit; ++r) {
+          if (r >= static_cast<int>(ranks)) break;
+          const float4 x = load_peer4(peer[r] + at);
+          v.x += x.x;
+          v.y += x.y;
+          v.z += x.z;
+          v.w += x.w;
+        }
       }
-    }
-    float f[4] = {v.x, v.y, v.z, v.w};
-    if (a.vec) {
+      float f[4] = {v.x, v.y, v.z, v.w};
       bad |= finish_row<4>(a.e, a.f16 != 0, m0 + line, n0 + j, f, bias, residual);
-    } else {
+    }
+  } else {
+    constexpr int kWarps = kProductThreads / 32, kRuns = (kLine + 127) / 128;  // a warp: 128 entries of a line
+    for (int i = warp + static_cast<int>(rank) * kWarps; i < lines * kRuns; i += static_cast<int>(ranks) * kWarps) {
+      const int line = i / kRuns, j = i % kRuns * 128 + lane;
+      bool in[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (j + k < len) bad |= finish(a.e, a.f16 != 0, m0 + line, n0 + j + k, f[k]);
+      for (int k = 0; k < 4; ++k) in[k] = j + 32 * k < len;
+      if (!in[0]) continue;
+      float bias[4] = {}, residual[4] = {}, f[4] = {};
+      if (a.e.bias != nullptr) load_apart(a.e.bias, a.e.bias_dtype, n0 + j, in, bias);
+      if (a.e.residual != nullptr)
+        load_apart(a.e.residual, a.e.residual_dtype, (m0 + line) * a.e.ld_residual + n0 + j, in, residual);
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r) {
+        if (r >= static_cast<int>(ranks)) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (in[k]) f[k] += load_peer(peer[r] + 4 * (line * kLineLd + j + 32 * k));
+      }
+      bad |= finish_apart(a.e, a.f16 != 0, m0 + line, n0 + j, in, f, bias, residual);
     }
   }
   if (bad) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
@@ -876,8 +942,8 @@ __global__ void __launch_bounds__(256) no_depth_kernel(const __grid_constant__ P
 }
 
 // Matrices whose rows start off the 16-byte grid, copied to rows that start on it: a
-// warp a row at a time, in eight-entry pieces of the copy.  The reads are single
-// entries, but neighbouring ones, which L1 gathers.
+// warp a row at a time, in 16-byte pieces of the copy, each shifted together from the
+// two 16-byte pieces of the row that it lies across.
 struct PackArgs {
   const uint16_t* x[2];
   uint16_t* y[2];
@@ -893,15 +959,30 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
     const uint16_t* x = one ? a.x[0] + row * a.ldx[0] : a.x[1] + row * a.ldx[1];
     uint16_t* y = one ? a.y[0] + row * a.ldy[0] : a.y[1] + row * a.ldy[1];
     const int cols = one ? a.cols[0] : a.cols[1];
+    // bytes that the row starts behind the grid, alike for all lanes
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x) & 15u);
+    const uint4* grid = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x) - off);
+    const int bytes = 2 * cols;
 #pragma unroll 2
-    for (int c = 8 * lane; c < cols; c += 256) {
-      uint32_t w[4];
+    for (int c = 16 * lane; c < bytes; c += 512) {
+      // pieces that hold a byte of the row (a piece never leaves the row's allocation)
+      const uint4 a0 = grid[c / 16];
+      const uint4 a1 = off != 0 && c + 16 - static_cast<int>(off) < bytes ? grid[c / 16 + 1] : make_uint4(0, 0, 0, 0);
+      const uint32_t w[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      uint32_t v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = c + 2 * k < cols ? x[c + 2 * k] : 0, hi = c + 2 * k + 1 < cols ? x[c + 2 * k + 1] : 0;
-        w[k] = lo | hi << 16;
+        uint32_t lo = w[k], hi = w[k + 1];
+        if (off >= 4) lo = w[k + 1], hi = w[k + 2];
+        if (off >= 8) lo = w[k + 2], hi = w[k + 3];
+        if (off >= 12) lo = w[k + 3], hi = k < 3 ? w[k + 4] : w[7];
+        v[k] = (off & 2u) != 0 ? __funnelshift_r(lo, hi, 16) : lo;
       }
-      *reinterpret_cast<uint4*>(y + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      const int left = bytes - c;  // zeros behind the row
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (left < 4 * k + 4) v[k] = left > 4 * k ? v[k] & 0xFFFFu : 0u;
+      *reinterpret_cast<uint4*>(y + c / 2) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
 }
@@ -986,7 +1067,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, i
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + col;
   double t = 0.0;
   if (j < n)
-#pragma unroll 4
+#pragma unroll 8
     for (int b = part; b < blocks; b += 8) t += partial[static_cast<int64_t>(b) * n + j];
   sums[part][col] = t;
   __syncthreads();

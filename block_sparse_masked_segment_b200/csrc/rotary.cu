@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(1024) head_grad_sum_kernel(const HeadArgs a, i
   const int i = static_cast<int>(blockIdx.x) * 32 + col;
   double t = 0.0;
   if (i < a.d)
+#pragma unroll 10
     for (int b = part; b < blocks; b += 32) t += s.partial[static_cast<int64_t>(b) * a.d + i];
   sums[part][col] = t;
   __syncthreads();
@@ -580,10 +581,14 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
     for (int i = 0; i < 8; ++i) *reinterpret_cast<uint64_t*>(mine + at[2 * i / VW] + 2 * i % VW) = acc[i];
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.d; e += kThreadsVec) {
+  // four threads to an entry, a quarter of the groups each
+  for (int e = threadIdx.x / 4; e < a.d; e += kThreadsVec / 4) {
     float t = 0.f;
-    for (int g = 0; g < kGroups; ++g) t += red[g * a.d + e];
-    s.partial[static_cast<int64_t>(block) * a.d + e] = t;
+#pragma unroll
+    for (int g = 0; g < kGroups / 4; ++g) t += red[(threadIdx.x % 4 * (kGroups / 4) + g) * a.d + e];
+    t += __shfl_xor_sync(0xffffffffu, t, 1);
+    t += __shfl_xor_sync(0xffffffffu, t, 2);
+    if (threadIdx.x % 4 == 0) s.partial[static_cast<int64_t>(block) * a.d + e] = t;
   }
 }
 
