@@ -233,11 +233,14 @@ __device__ __forceinline__ Raw<T> load_unit(const T* p, const UnitAt<VW>& at) {
       r.w[2 * q] = v.x;
       r.w[2 * q + 1] = v.y;
     } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(p + at[q]);
-      r.w[4 * q] = v.x;
-      r.w[4 * q + 1] = v.y;
-      r.w[4 * q + 2] = v.z;
-      r.w[4 * q + 3] = v.w;
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p + at[q])[i];
+        r.w[kWords * q + 4 * i] = v.x;
+        r.w[kWords * q + 4 * i + 1] = v.y;
+        r.w[kWords * q + 4 * i + 2] = v.z;
+        r.w[kWords * q + 4 * i + 3] = v.w;
+      }
     }
   }
   return r;
@@ -325,32 +328,44 @@ __device__ __forceinline__ void read16(const float4* t, int units, int c, uint64
   }
 }
 
+// i / by through a product: exact while i * by < 2^32; magic 0 where the host cannot
+// promise that (or by is 1): the plain quotient.
+struct Quotient {
+  uint32_t by, magic;
+};
+__device__ __forceinline__ int quotient(int i, const Quotient& q) {
+  return q.magic != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), q.magic)) : i / static_cast<int>(q.by);
+}
 // cos and sin of `ntok` tokens from tok0 into cs [ntok][4][pairs / 8], in the order
-// of rotate_unit; the transpose's have the sine negated.
+// of rotate_unit; the transpose's have the sine negated.  `by_pairs`: quotient by pairs.
 template <int VW>
-__device__ __forceinline__ void fill_turns(const HeadArgs& a, int64_t tok0, int ntok, bool transpose, float4* cs) {
+__device__ __forceinline__ void fill_turns(const HeadArgs& a, const Quotient& by_pairs, int64_t tok0, int ntok,
+                                           bool transpose, float4* cs) {
   const int units = a.pairs / 8;
   const int per = a.interleaved ? VW / 2 : VW;  // pairs that a vector (of the first halves) begins
-  const int span = units * per;                 // pairs that one vector of each lane begins
-  for (int i = threadIdx.x; i < ntok * a.pairs; i += blockDim.x) {
-    const int t = i / a.pairs, j = i % a.pairs;
+  const int span = units * per;                 // pairs that one vector of each lane begins: all, 1/2 or 1/4
+  for (int i = threadIdx.x; i < ntok * a.pairs; i += kThreadsVec) {
+    const int t = quotient(i, by_pairs), j = i - t * a.pairs;
     float c, s;
     turn(a.pos[tok0 + t], a.freq[j], a.scale, c, s);
-    const int unit = j % span / per, slot = j / span * per + j % per;
+    const int seg = (j >= span) + (j >= 2 * span) + (j >= 3 * span), k = j - seg * span;
+    const int shift = per == 8 ? 3 : per == 4 ? 2 : 1;
+    const int unit = k >> shift, slot = seg * per + (k & (per - 1));
     float* to = reinterpret_cast<float*>(cs + (t * 4 + slot / 2) * units + unit) + (slot & 1);
     to[0] = c;
     to[2] = transpose ? -s : s;
   }
 }
 
-// The unit's entries of a weight.
+// The unit's entries of a weight (16-byte aligned).
 template <int VW>
 __device__ __forceinline__ void load_weight(const HeadArgs& a, const void* w, const UnitAt<VW>& at, uint64_t (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = at[2 * i / VW] + 2 * i % VW;
-    f[i] = f2(load_typed(w, a.w_dtype, e), load_typed(w, a.w_dtype, e + 1));
-  }
+  if (a.w_dtype == OPR_DTYPE_BF16)
+    unpack(load_unit(static_cast<const __nv_bfloat16*>(w), at), f);
+  else if (a.w_dtype == OPR_DTYPE_FP16)
+    unpack(load_unit(static_cast<const __half*>(w), at), f);
+  else
+    unpack(load_unit(static_cast<const float*>(w), at), f);
 }
 
 template <int G>
@@ -366,22 +381,16 @@ __device__ __forceinline__ float sum2(uint64_t v) {
   return lo + hi;
 }
 
-// i / heads for i < tokens * heads, by a product: exact while i * heads < 2^32, which
-// the callers' choice of the tokens keeps (else the plain quotient).
-struct Quotient {
-  uint32_t heads, magic;
-};
-__device__ __forceinline__ int quotient(int i, const Quotient& q) {
-  return q.magic != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), q.magic)) : i / static_cast<int>(q.heads);
-}
 struct Quotients {
-  Quotient set[3];
+  Quotient set[3];  // by the set's heads
+  Quotient pairs;
 };
 
 // A block takes `tokens` tokens, forms their cos and sin once, and its groups of G
 // lanes walk each set's (token, head) items in rounds, the next round's loads in
 // flight.
-template <typename TI, typename TO, int VW, int G>
+// NORM: the sets of opr_qk_norm_rope; else the one set of opr_rotary.
+template <typename TI, typename TO, int VW, int G, bool NORM>
 __global__ void __launch_bounds__(kThreadsVec, 4) heads_vec_kernel(const HeadArgs a, const Quotients quot, int32_t tokens) {
   constexpr int kGroups = kThreadsVec / G;
   extern __shared__ float4 tables[];
@@ -395,21 +404,21 @@ __global__ void __launch_bounds__(kThreadsVec, 4) heads_vec_kernel(const HeadArg
   const UnitAt<VW> at(a, live ? c : 0);
   const float inv_d = 1.f / a.d;
 
-  int si = 0, base = 0;  // the round's set and its first item (both uniform in the block)
+  int si = 0, base = 0;  // the round's set (0 without NORM) and its first item, uniform in the block
   Raw<TI> raw{};
   int t = 0, h = 0;
   bool valid = false;
   auto fetch = [&]() {
-    const HeadSet& s = a.set[si];
+    const HeadSet& s = a.set[NORM ? si : 0];
     const int i = base + group;
-    t = quotient(i, quot.set[si]);
+    t = quotient(i, quot.set[NORM ? si : 0]);
     h = i - t * s.heads;
     valid = live && t < ntok;
     if (valid)
       raw = load_unit(static_cast<const TI*>(s.x) + (tok0 + t) * s.x_stride + static_cast<int64_t>(h) * a.d, at);
   };
   fetch();  // in flight while the tables are made
-  fill_turns<VW>(a, tok0, ntok, a.inverse != 0, cs);
+  fill_turns<VW>(a, quot.pairs, tok0, ntok, a.inverse != 0, cs);
   bool lost = false;
   for (int i = threadIdx.x; i < ntok; i += kThreadsVec) {
     const int64_t r = a.row_map != nullptr ? a.row_map[tok0 + i] : tok0 + i;
@@ -420,9 +429,9 @@ __global__ void __launch_bounds__(kThreadsVec, 4) heads_vec_kernel(const HeadArg
   __syncthreads();
   __half2 top = __float2half2_rn(0.f);
   uint64_t w[8];
-  if (a.set[0].mode == kHeadNormRotate) load_weight(a, a.set[0].w, at, w);
+  if (NORM) load_weight(a, a.set[0].w, at, w);
   while (true) {
-    const HeadSet& s = a.set[si];
+    const HeadSet& s = a.set[NORM ? si : 0];
     uint64_t x[8];
     unpack(raw, x);
     const int now_t = t, now_h = h, now_si = si;
@@ -432,9 +441,9 @@ __global__ void __launch_bounds__(kThreadsVec, 4) heads_vec_kernel(const HeadArg
       base = 0;
       ++si;
     }
-    const bool more = si < a.n_sets;
+    const bool more = si < (NORM ? a.n_sets : 1);
     if (more) fetch();
-    if (s.mode == kHeadNormRotate) {
+    if (NORM && s.mode == kHeadNormRotate) {
       uint64_t sq = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sq = ffma2(x[i], x[i], sq);
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(kThreadsVec, 4) heads_vec_kernel(const HeadArg
     }
     const int to = now_valid ? orow[now_t] : -1;
     if (to >= 0) {
-      if (turns && s.mode != kHeadCopy) {
+      if (turns && (!NORM || s.mode != kHeadCopy)) {
         uint64_t cw[8];
         read16(cs + now_t * 4 * rot_units, rot_units, c, cw);
         if (a.interleaved)
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(kThreadsVec, 4) heads_vec_kernel(const HeadArg
       store_unit(static_cast<TO*>(s.y) + to * s.y_stride + static_cast<int64_t>(now_h) * a.d, at, x, top);
     }
     if (!more) break;
-    if (si != now_si && a.set[si].mode == kHeadNormRotate) load_weight(a, a.set[si].w, at, w);
+    if (NORM && si != now_si && a.set[si].mode == kHeadNormRotate) load_weight(a, a.set[si].w, at, w);
   }
   if (a.dev_status != nullptr) {
     if (overflowed(top)) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
@@ -527,7 +536,7 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
     fetch(group);
     if (!copy) {
       __syncthreads();  // the tile before has been read
-      fill_turns<VW>(a, tok0, ntok, true, cs);
+      fill_turns<VW>(a, quot.pairs, tok0, ntok, true, cs);
       __syncthreads();
     }
     for (int base = 0; base < items; base += kGroups) {
@@ -607,7 +616,8 @@ bool vector_ready(const HeadArgs& a, int32_t x_dtype, int32_t dy_dtype, int32_t 
   };
   for (int i = 0; i < a.n_sets; ++i) {
     const HeadSet& s = a.set[i];
-    if (!fits(s.x, s.x_stride, x_dtype) || !fits(s.dy, s.dy_stride, dy_dtype) || !fits(s.y, s.y_stride, y_dtype))
+    if (!fits(s.x, s.x_stride, x_dtype) || !fits(s.dy, s.dy_stride, dy_dtype) || !fits(s.y, s.y_stride, y_dtype) ||
+        !fits(s.w, 0, a.w_dtype))
       return false;
   }
   return true;
@@ -625,18 +635,23 @@ cudaError_t with_group(int32_t d, F f) {
   return f(std::integral_constant<int, 16>{});
 }
 
-// Quotients by the sets' heads for items of up to `tokens` tokens.
+// Quotient for numbers below `most`.
+Quotient quotient_by(int32_t by, int64_t most) {
+  Quotient q{static_cast<uint32_t>(by), 0};
+  if (by > 1 && most * by < (int64_t{1} << 32)) q.magic = static_cast<uint32_t>(((uint64_t{1} << 32) + q.by - 1) / q.by);
+  return q;
+}
+
+// Those of tiles of tokens[i] tokens of set i; items of the last round may reach past
+// the tile by a round of groups.
 Quotients quotients(const HeadArgs& a, const int32_t (&tokens)[3]) {
   Quotients q{};
+  int32_t most = 0;
   for (int i = 0; i < a.n_sets; ++i) {
-    const uint64_t heads = static_cast<uint64_t>(a.set[i].heads);
-    q.set[i].heads = static_cast<uint32_t>(heads);
-    // items of the last round may reach past the tokens by a round of groups
-    const uint64_t items = static_cast<uint64_t>(tokens[i]) * heads + 2 * kThreadsVec;
-    q.set[i].magic = heads > 1 && items * heads < (uint64_t{1} << 32)
-                         ? static_cast<uint32_t>(((uint64_t{1} << 32) + heads - 1) / heads)
-                         : 0;
+    q.set[i] = quotient_by(a.set[i].heads, static_cast<int64_t>(tokens[i]) * a.set[i].heads + 2 * kThreadsVec);
+    most = std::max(most, tokens[i]);
   }
+  q.pairs = quotient_by(a.pairs, static_cast<int64_t>(most) * a.pairs + kThreadsVec);
   return q;
 }
 
@@ -660,7 +675,13 @@ cudaError_t launch_heads_vec(const HeadArgs& a, int32_t x_dtype, int32_t y_dtype
     const Quotients q = quotients(a, each);
     return with_type(x_dtype, [&](auto ti) {
       return with_type(y_dtype, [&](auto to) {
-        heads_vec_kernel<decltype(ti), decltype(to), vector_width<decltype(ti), decltype(to)>, G><<<blocks, kThreadsVec, smem, stream>>>(a, q, tokens);
+        using TI = decltype(ti);
+        using TO = decltype(to);
+        constexpr int VW = vector_width<TI, TO>;
+        if (a.set[0].mode == kHeadNormRotate)
+          heads_vec_kernel<TI, TO, VW, G, true><<<blocks, kThreadsVec, smem, stream>>>(a, q, tokens);
+        else
+          heads_vec_kernel<TI, TO, VW, G, false><<<blocks, kThreadsVec, smem, stream>>>(a, q, tokens);
         return cudaGetLastError();
       });
     });
