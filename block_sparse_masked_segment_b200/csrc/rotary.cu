@@ -501,10 +501,22 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
   const bool live = c < units, turns = c < rot_units && !copy;
   const UnitAt<VW> at(a, live ? c : 0);
   const float inv_d = 1.f / a.d;
-  uint64_t acc[8], w[8];
+  uint64_t acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0;
-  if (!copy) load_weight(a, s.w, at, w);
+  // the weight, for the lanes to read back by unit: registers for it would spill
+  float4* wt = reinterpret_cast<float4*>(red + kGroups * a.d);  // [4][units]
+  if (!copy && threadIdx.x < G && live) {
+    uint64_t w[8];
+    load_weight(a, s.w, at, w);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      ulonglong2 pair;
+      pair.x = w[2 * q];
+      pair.y = w[2 * q + 1];
+      *reinterpret_cast<ulonglong2*>(wt + q * units + c) = pair;
+    }
+  }
   __half2 top = __float2half2_rn(0.f);
   bool lost = false;
 
@@ -556,7 +568,8 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
       }
       if (!copy) {
         // sums of x^2 and of u x in one round of shuffles (u = g w); xh = x rs after it
-        uint64_t u[8], sq = 0, ux = 0;
+        uint64_t w[8], u[8], sq = 0, ux = 0;
+        read16(wt, units, live ? c : 0, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           u[i] = fmul2(g[i], w[i]);
@@ -705,18 +718,23 @@ cudaError_t launch_heads(const HeadArgs& a, int32_t x_dtype, int32_t y_dtype, cu
 }
 
 namespace {
-constexpr int32_t kGradBlocks = 4 * 148;   // at most, per set
-constexpr int32_t kVecGradBlocks = 2 * 148;  // over all sets: what runs at one time
+constexpr int32_t kGradBlocks = 16 * 148;  // at most
 
 cudaError_t launch_head_grads_vec(const HeadArgs& a, int32_t x_dtype, int32_t dy_dtype, int32_t dx_dtype,
                                   int32_t (&blocks)[3], cudaStream_t stream) {
   // v counted whether it is there or not: the sums for w do not depend on it
   const int32_t heads = a.set[0].heads + 2 * a.set[1].heads;
   GradBlocks deal{};
+  // Blocks over all sets: about 40 rounds of items to each, from the two to an SM that
+  // run at one time up to eight times as many, which even the sets' speeds out (64K
+  // tokens of 64q/8kv heads of 128: 1050 us with 296, 885 with 592, 842 with 2368;
+  // 2377 tokens of 8q/2kv heads of 64: 13 with 296, 44 with 2368).
+  const int64_t rounds = a.total * heads * (a.d / 16) / kThreadsVec;
+  const int64_t total_blocks = std::max<int64_t>(2 * 148, std::min<int64_t>(kGradBlocks, rounds / 40));
   for (int i = 0; i < 3; ++i) {
     int64_t n = 0;
     if (i < a.n_sets) {
-      n = std::max<int64_t>(1, (static_cast<int64_t>(kVecGradBlocks) * a.set[i].heads + heads / 2) / heads);
+      n = std::max<int64_t>(1, (total_blocks * a.set[i].heads + heads / 2) / heads);
       n = std::min<int64_t>(n, a.total);
     }
     blocks[i] = static_cast<int32_t>(n);
@@ -733,7 +751,7 @@ cudaError_t launch_head_grads_vec(const HeadArgs& a, int32_t x_dtype, int32_t dy
     }
     deal.cs_bytes = static_cast<int32_t>(sizeof(float4)) * most * 4 * (a.pairs / 8);
     const Quotients q = quotients(a, deal.tokens);
-    const size_t smem = deal.cs_bytes + sizeof(float) * (kThreadsVec / G) * a.d;
+    const size_t smem = deal.cs_bytes + sizeof(float) * (kThreadsVec / G + 1) * a.d;
     return with_type(x_dtype, [&](auto ti) {
       return with_type(dy_dtype, [&](auto tg) {
         return with_type(dx_dtype, [&](auto to) {
@@ -770,7 +788,7 @@ cudaError_t launch_head_grads(const HeadArgs& a, int32_t x_dtype, int32_t dy_dty
       int32_t heads = 0;
       for (int i = 0; i < a.n_sets; ++i) heads = std::max(heads, a.set[i].heads);
       blocks[0] = blocks[1] =
-          static_cast<int32_t>(std::min<int64_t>(kGradBlocks, (a.total * heads + kWarps - 1) / kWarps));
+          static_cast<int32_t>(std::min<int64_t>(4 * 148, (a.total * heads + kWarps - 1) / kWarps));
       e = with_type(x_dtype, [&](auto ti) {
         return with_type(dy_dtype, [&](auto tg) {
           return with_type(dx_dtype, [&](auto to) {
