@@ -14,6 +14,7 @@ namespace opr {
 namespace {
 
 constexpr int64_t kMaxRows = int64_t{1} << 31;
+constexpr int32_t kMaxHeads = 65536;
 
 // A strided block of rows in memory.
 struct Rows {
@@ -100,7 +101,11 @@ PackJob pack(Operand& o, int64_t rows, int32_t cols, void* to) {
   return job;
 }
 
-bool linear_sizes_ok(int64_t m, int32_t n, int32_t k) { return m >= 0 && m < kMaxRows && n > 0 && k > 0; }
+// Coordinates of whole tiles past the ends stay within int32.
+constexpr int64_t kMaxExtent = kMaxRows - 512;
+bool linear_sizes_ok(int64_t m, int32_t n, int32_t k) {
+  return m >= 0 && m <= kMaxExtent && n > 0 && n <= kMaxExtent && k > 0 && k <= kMaxExtent;
+}
 bool known_act(int32_t a) { return a >= OPR_ACT_NONE && a <= OPR_ACT_GELU_TANH; }
 
 }  // namespace
@@ -153,10 +158,10 @@ opr_status opr_rotary(const void* x, int32_t x_dtype, int64_t x_stride, void* y,
                       int32_t inverse, const int32_t* row_map, int64_t total_tokens, int32_t n_heads,
                       int32_t head_dim, int32_t* dev_status, void* stream) {
   CallRange range("opr_rotary");
-  if (!head_args_ok(total_tokens, head_dim, rot_dim, scale) || n_heads < 0) return OPR_INVALID_ARG;
+  if (!head_args_ok(total_tokens, head_dim, rot_dim, scale) || n_heads < 0 || n_heads > kMaxHeads) return OPR_INVALID_ARG;
   if (!known_dtype(x_dtype) || !known_dtype(y_dtype)) return OPR_UNSUPPORTED;
   const int64_t width = static_cast<int64_t>(n_heads) * head_dim;
-  if (width >= kMaxRows || x_stride < width || y_stride < width) return OPR_INVALID_ARG;
+  if (x_stride < width || y_stride < width) return OPR_INVALID_ARG;
   if (total_tokens == 0 || n_heads == 0) return OPR_OK;
   if (!x || !y || !pos_id || !freq || !element_aligned(x, x_dtype) || !element_aligned(y, y_dtype))
     return OPR_INVALID_ARG;
@@ -184,11 +189,12 @@ opr_status opr_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
                             int32_t hkv, int32_t head_dim, void* q_out, void* k_out, void* v_out, int32_t y_dtype,
                             int32_t* dev_status, void* stream) {
   CallRange range("opr_qk_norm_rope");
-  if (!head_args_ok(total_tokens, head_dim, rot_dim, scale) || hq <= 0 || hkv <= 0) return OPR_INVALID_ARG;
+  if (!head_args_ok(total_tokens, head_dim, rot_dim, scale) || hq <= 0 || hkv <= 0 || hq > kMaxHeads || hkv > kMaxHeads)
+    return OPR_INVALID_ARG;
   if (!known_dtype(x_dtype) || !known_dtype(y_dtype) || !known_dtype(w_dtype)) return OPR_UNSUPPORTED;
   if (!(eps > 0.f) || !std::isfinite(eps)) return OPR_INVALID_ARG;
   const int64_t wq = static_cast<int64_t>(hq) * head_dim, wkv = static_cast<int64_t>(hkv) * head_dim;
-  if (wq >= kMaxRows || wkv >= kMaxRows || q_stride < wq || k_stride < wkv || (v && v_stride < wkv))
+  if (q_stride < wq || k_stride < wkv || (v && v_stride < wkv))
     return OPR_INVALID_ARG;
   if ((v == nullptr) != (v_out == nullptr)) return OPR_INVALID_ARG;
   if (total_tokens == 0) return OPR_OK;
@@ -245,12 +251,13 @@ opr_status opr_qk_norm_rope_bwd(const void* dq, const void* dk, const void* dv, 
                                 void* dv_out, int64_t dv_stride, int32_t dx_dtype, float* dq_weight, float* dk_weight,
                                 void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
   CallRange range("opr_qk_norm_rope_bwd");
-  if (!head_args_ok(total_tokens, head_dim, rot_dim, scale) || hq <= 0 || hkv <= 0) return OPR_INVALID_ARG;
+  if (!head_args_ok(total_tokens, head_dim, rot_dim, scale) || hq <= 0 || hkv <= 0 || hq > kMaxHeads || hkv > kMaxHeads)
+    return OPR_INVALID_ARG;
   if (!known_dtype(x_dtype) || !known_dtype(dy_dtype) || !known_dtype(dx_dtype) || !known_dtype(w_dtype))
     return OPR_UNSUPPORTED;
   if (!(eps > 0.f) || !std::isfinite(eps)) return OPR_INVALID_ARG;
   const int64_t wq = static_cast<int64_t>(hq) * head_dim, wkv = static_cast<int64_t>(hkv) * head_dim;
-  if (wq >= kMaxRows || wkv >= kMaxRows || q_stride < wq || k_stride < wkv || dq_stride < wq || dk_stride < wkv ||
+  if (q_stride < wq || k_stride < wkv || dq_stride < wq || dk_stride < wkv ||
       (dv && dv_stride < wkv))
     return OPR_INVALID_ARG;
   if ((dv == nullptr) != (dv_out == nullptr)) return OPR_INVALID_ARG;

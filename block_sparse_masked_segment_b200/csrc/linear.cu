@@ -145,7 +145,7 @@ struct ProductArgs {
   int64_t depth;
   int32_t f16;
   int32_t folded_p, folded_q;  // MN-major operands: the map is of chunks (load_slice)
-  int32_t tiles_p, tiles_q;    // product_pair_kernel
+  int32_t tiles_p, tiles_q;    // tiles along P and, product_pair_kernel only, Q
   int32_t vec;  // the rows of y, z and the residual allow vector accesses
   LinearEpilogue e;
   int32_t* dev_status;
@@ -384,8 +384,9 @@ __global__ void __launch_bounds__(kProductThreads, 2)
   Smem& sm = *reinterpret_cast<Smem*>(align1024(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x / ranks) * kRowsP;
-  const int q0 = blockIdx.y * BN;
+  const int tile = static_cast<int>(blockIdx.x / ranks);
+  const int64_t p0 = static_cast<int64_t>(tile % a.tiles_p) * kRowsP;
+  const int q0 = tile / a.tiles_p * BN;
   const int64_t slices = (a.depth + kDepth - 1) / kDepth;
   const int s0 = static_cast<int>(slices * rank / ranks), s1 = static_cast<int>(slices * (rank + 1) / ranks);
   const int n = s1 - s0;
@@ -628,7 +629,8 @@ __device__ __forceinline__ void stage_row32(uint8_t* block, int row, const float
         make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
 }
 
-// A lane's row of a residual block, as loaded; columns past the end are not read.
+// A lane's row of a residual block, as loaded; columns past the end (a multiple of
+// eight) are not read.
 struct RawRow {
   uint4 v[8];
 };
@@ -639,19 +641,7 @@ __device__ __forceinline__ void fetch_residual(const LinearEpilogue& e, int64_t 
 #pragma unroll
   for (int g = 0; g < 8; ++g) {
     raw.v[g] = make_uint4(0, 0, 0, 0);
-    if (!wide && g >= 4) continue;
-    if (n0 + per * (g + 1) <= cols) {
-      raw.v[g] = reinterpret_cast<const uint4*>(p)[g];
-    } else if (n0 + per * g < cols) {  // the row's last entries
-      uint32_t w[4] = {0, 0, 0, 0};
-      for (int k = 0; k < per && n0 + per * g + k < cols; ++k) {
-        if (wide)
-          w[k] = reinterpret_cast<const uint32_t*>(p)[per * g + k];
-        else
-          w[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[per * g + k]) << (16 * (k & 1));
-      }
-      raw.v[g] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    if ((wide || g < 4) && n0 + per * g < cols) raw.v[g] = reinterpret_cast<const uint4*>(p)[g];
   }
 }
 __device__ __forceinline__ void add_residual(const RawRow& raw, int32_t dtype, float (&v)[32]) {
@@ -799,7 +789,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     }
   } else {
     // A warp finishes 32 rows (one a lane) x 128 columns of the CTA's tile in chunks of
-    // 32 columns: in registers, then staged and stored by TMA, which clips the ends.
+    // 32 columns: in registers, then staged and stored by TMA, which leaves the ends off.
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     uint8_t* stage = sm.stage[warp - 2];
@@ -1165,7 +1155,8 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cuda
   const int split = tile_split(tiles, slices);
   a.vec = rows_aligned(a.e) && (SWAP ? a.rows_p : a.rows_q) % 4 == 0 && reinterpret_cast<uintptr_t>(a.e.bias) % 16 == 0;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles_p * split), static_cast<unsigned>(tiles_q));
+  a.tiles_p = static_cast<int32_t>(tiles_p);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
   cfg.blockDim = dim3(kProductThreads);
   cfg.dynamicSmemBytes = kTileSmem;
   cfg.stream = stream;
@@ -1188,7 +1179,8 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cuda
   if (e != cudaSuccess) return e;
   a.tiles_p = static_cast<int32_t>(ceil_div(a.rows_p, kPairTile));
   a.tiles_q = static_cast<int32_t>(ceil_div(a.rows_q, kPairTile));
-  a.vec = rows_aligned(a.e);
+  // a row that ends inside 16 bytes would be stored up to their end
+  a.vec = rows_aligned(a.e) && a.rows_q % 8 == 0;
   CUtensorMap my = mp, mz = mp;  // not used where the epilogue is entry by entry, or without z
   if (a.vec && (!block_map(&my, a.e.y, a.e.ldy, a.e.y_dtype, a.rows_p, a.rows_q) ||
                 (a.e.z != nullptr && !block_map(&mz, a.e.z, a.e.ldz, a.f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, a.rows_p, a.rows_q))))

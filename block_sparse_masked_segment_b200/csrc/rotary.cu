@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(32 * kWarps) heads_kernel(const HeadArgs a, in
   };
   bool bad = false;
   auto put = [&](int i, float v) {
-    bad |= beyond<TO>(v);
     y[i] = from_float<TO>(v);
+    bad |= beyond<TO>(as_float(y[i]));
   };
   const int pairs = s.mode == kHeadCopy ? 0 : a.pairs;
   for (int j = lane; j < pairs; j += 32) {
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(32 * kWarps) head_grads_kernel(const HeadArgs 
     const TG* dy = static_cast<const TG*>(s.dy) + grow * s.dy_stride + static_cast<int64_t>(h) * a.d;
     TO* dx = static_cast<TO*>(s.y) + tok * s.y_stride + static_cast<int64_t>(h) * a.d;
     auto put = [&](int i, float v) {
-      bad |= beyond<TO>(v);
       dx[i] = from_float<TO>(v);
+      bad |= beyond<TO>(as_float(dx[i]));
     };
     if (s.mode == kHeadCopy) {
       for (int i = lane; i < a.d; i += 32) put(i, as_float(dy[i]));

@@ -559,7 +559,7 @@ OPR_API opr_status opr_rotary_frequencies(int32_t rot_dim, double base, int32_t 
  *             range sets OPR_DEV_BAD_INPUT and its row is not written.
  *   dev_status  may be NULL; otherwise also OPR_DEV_FP16_RANGE when an fp16 output overflows
  * y may be x (same type and stride, no row_map); any other overlap is refused.  head_dim 2 .. 256,
- * rot_dim even, 2 .. head_dim.  opr_rope is the case of the whole head, the half layout and
+ * rot_dim even, 2 .. head_dim, at most 65536 heads.  opr_rope is the case of the whole head, the half layout and
  * OPR_ROTARY_PLAIN.
  */
 OPR_API opr_status opr_rotary(const void* x, int32_t x_dtype, int64_t x_stride, void* y, int32_t y_dtype,
@@ -631,7 +631,7 @@ OPR_API opr_status opr_qk_norm_rope_bwd(const void* dq, const void* dk, const vo
  *   workspace 16-byte aligned, may be NULL when 0 bytes are needed; calls that may run at the same
  *             time need workspaces of their own
  *   dev_status required: OPR_DEV_WAIT_TIMEOUT, OPR_DEV_FP16_RANGE (an fp16 y or z overflows)
- * m = 0 does nothing; n, k > 0; m < 2^31.  Outputs that overlap inputs or one another are refused.
+ * m = 0 does nothing; n, k > 0; all at most 2^31 - 512.  Outputs that overlap inputs or one another are refused.
  */
 #define OPR_ACT_NONE 0
 #define OPR_ACT_SILU 1

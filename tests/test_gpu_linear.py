@@ -135,6 +135,35 @@ def test_linear_on_parts_of_wider_rows(wide, offset):
         assert (t[rest] == 5).all()
 
 
+@pytest.mark.parametrize("n,k", [(72, 101), (71, 100), (70, 99), (69, 98), (68, 97), (65, 66)])
+@pytest.mark.parametrize("m", [5, 150, 2400])
+def test_linear_rows_that_end_inside_sixteen_bytes(m, n, k):
+    """Rows that start on the 16-byte grid (and so are read in place) but end off it, NaN right behind them
+    in every operand: nothing of it reaches a sum, and nothing is written behind the results' ends."""
+    rng = np.random.default_rng(18)
+    if m == 2400:
+        n += 2296  # many tiles: the CTA pairs
+
+    def inside(rows, cols, dtype, fill=float("nan")):
+        t = torch.full((rows, (cols + 7) // 8 * 8 + 8), fill, dtype=TYPES[dtype], device="cuda")
+        v = t[:, :cols]
+        v.copy_(matrix(rng, rows, cols, dtype))
+        return t, v
+
+    (_, x), (_, w), (_, r), (_, dy) = (inside(*a, "bf16") for a in ((m, k), (n, k), (m, n), (m, n)))
+    ty, y = inside(m, n, "bf16", 5.0)
+    opr.opr_linear(x, w, residual=r, out=y)
+    ref = to64(x) @ to64(w).T + to64(r)
+    within(y, ref, sum_bound(to64(x), to64(w), k) + np.abs(ref) * 2.0 ** -23, "bf16")
+    (tdx, dx), (tdw, dw) = inside(m, k, "bf16", 5.0), inside(n, k, "bf16", 5.0)
+    _, _, db = opr.opr_linear_bwd(dy, x, w, bias=True, out=(dx, dw))
+    within(dx, to64(dy) @ to64(w), sum_bound(to64(dy), to64(w).T, n), "bf16")
+    within(dw, to64(dy).T @ to64(x), sum_bound(to64(dy).T, to64(x).T, m), "bf16")
+    within(db, to64(dy).sum(0), np.abs(to64(dy)).sum(0) * 2.0 ** -14, "fp32")
+    for t, v in ((ty, y), (tdx, dx), (tdw, dw)):
+        assert (t[:, v.shape[1]:] == 5).all()
+
+
 def test_linear_into_its_residual():
     rng = np.random.default_rng(5)
     x, w, r = matrix(rng, 300, 128, "bf16"), matrix(rng, 200, 128, "bf16"), matrix(rng, 300, 200, "fp32")
@@ -145,6 +174,29 @@ def test_linear_into_its_residual():
     want, _, _ = opr.opr_linear_bwd(dy, x, w, dx_residual=add, need_dw=False)
     got, dw, db = opr.opr_linear_bwd(dy, x, w, dx_residual=add, need_dw=False, out=(add, None))
     assert got is add and dw is None and db is None and torch.equal(got, want)
+
+
+def test_large_products_into_their_residual():
+    rng = np.random.default_rng(17)
+    x, w, r = matrix(rng, 2500, 64, "bf16"), matrix(rng, 2304, 64, "bf16"), matrix(rng, 2500, 2304, "bf16")
+    want = opr.opr_linear(x, w, residual=r)
+    assert torch.equal(opr.opr_linear(x, w, residual=r, out=r), want)
+    r32 = matrix(rng, 2500, 2304, "fp32")
+    want = opr.opr_linear(x, w, residual=r32, out_dtype=torch.float32)
+    assert torch.equal(opr.opr_linear(x, w, residual=r32, out=r32), want)
+
+
+@pytest.mark.parametrize("m", [2, 100])
+def test_linear_with_very_many_columns(m):
+    """More tiles along n than a grid has rows; offsets of y and w past 2^31 bytes."""
+    n, k = 64 * 65535 * (8 if m == 2 else 3) + 200, 8 if m == 100 else 40
+    g = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randn(m, k, device="cuda", dtype=torch.bfloat16, generator=g)
+    w = torch.randn(n, k, device="cuda", dtype=torch.bfloat16, generator=g)
+    y = opr.opr_linear(x, w)
+    for cols in (slice(0, 1000), slice(n // 2, n // 2 + 1000), slice(n - 1000, n)):
+        X, W = to64(x), to64(w[cols])
+        within(y[:, cols], X @ W.T, sum_bound(X, W, k), "bf16")
 
 
 def test_linear_keeps_infinities_and_nan_in_their_rows():
@@ -301,13 +353,14 @@ def test_large_epilogues(types, activation):
     block of 32 columns, and inside eight entries of it."""
     dtype, bt, rt, yt = types
     rng = np.random.default_rng(13)
-    for m, n, k in ((2500, 2076, 64), (2311, 2304, 72)):
+    for m, n, k in ((2500, 2075, 64), (2311, 2304, 72)):
         x, w = matrix(rng, m, k, dtype), matrix(rng, n, k, dtype, scale=2 * k ** -0.5)
         b = matrix(rng, 1, n, bt)[0] if bt else None
         ld = (n + 7) // 8 * 8
         r = matrix(rng, m, n, rt, wide=ld - n) if rt else None
         out = torch.full((m, ld), 5.0, dtype=TYPES[yt], device="cuda")
-        y, z = opr.opr_linear(x, w, b, activation, r, out=out[:, :n], save_z=True)
+        y = opr.opr_linear(x, w, b, activation, r, out=out[:, :n])
+        z = opr.opr_linear(x, w, b, activation, r, save_z=True)[1]
         assert (out[:, n:] == 5).all()
         ry, rz = lo.linear(to64(x), to64(w), 0 if b is None else to64(b), activation, None if r is None else to64(r))
         bz = sum_bound(to64(x), to64(w), k) + (np.abs(rz) + 2) * 2.0 ** -23

@@ -30,6 +30,7 @@ def rotary(lib, **kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(total=-1), INVALID), (dict(total=1 << 31), INVALID), (dict(heads=-1), INVALID),
+    (dict(heads=65537, xs=1 << 30, ys=1 << 30), INVALID),
     (dict(d=257, xs=514, ys=514), INVALID), (dict(rot=63), INVALID), (dict(rot=0), INVALID),
     (dict(rot=130), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(xs=255), INVALID), (dict(ys=255), INVALID), (dict(xt=3), UNSUPPORTED), (dict(yt=-1), UNSUPPORTED),
@@ -125,8 +126,8 @@ def lin(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(m=-1), INVALID), (dict(m=1 << 31), INVALID), (dict(n=0), INVALID), (dict(k=0), INVALID),
-    (dict(ldx=63), INVALID), (dict(ldw=63), INVALID), (dict(ldy=95), INVALID), (dict(ldr=95), INVALID),
+    (dict(m=-1), INVALID), (dict(m=(1 << 31) - 511), INVALID), (dict(n=0), INVALID), (dict(k=0), INVALID),
+    (dict(n=(1 << 31) - 511, ldy=1 << 31, ldr=1 << 31, ldz=1 << 31), INVALID), (dict(ldx=63), INVALID), (dict(ldw=63), INVALID), (dict(ldy=95), INVALID), (dict(ldr=95), INVALID),
     (dict(ldz=95), INVALID), (dict(act=4), UNSUPPORTED), (dict(act=-1), UNSUPPORTED), (dict(t=FP32), UNSUPPORTED),
     (dict(yt=5), UNSUPPORTED), (dict(bt=5), UNSUPPORTED), (dict(rt=5), UNSUPPORTED), (dict(x=None), INVALID),
     (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(st=None), INVALID),
