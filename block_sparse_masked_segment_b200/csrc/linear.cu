@@ -262,13 +262,14 @@ __device__ __forceinline__ void load_residual(const LinearEpilogue& e, int64_t m
   if (e.residual != nullptr) load_row<W>(e.residual, e.residual_dtype, m * e.ld_residual + n, v);
 }
 
-// Four entries of row m, 32 apart (neighbouring lanes take neighbouring ones), those of
-// `in` only: any alignment.  The loads go out together.
+// Four entries of row m, APART from one to the next (neighbouring lanes take neighbouring
+// ones), those of `in` only: any alignment.  The loads go out together.
+template <int APART>
 __device__ __forceinline__ void load_apart(const void* p, int32_t dtype, int64_t i, const bool (&in)[4], float (&v)[4]) {
   auto each = [&](auto type) {
     using T = decltype(type);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = in[k] ? as_float(static_cast<const T*>(p)[i + 32 * k]) : 0.f;
+    for (int k = 0; k < 4; ++k) v[k] = in[k] ? as_float(static_cast<const T*>(p)[i + APART * k]) : 0.f;
   };
   if (dtype == OPR_DTYPE_BF16)
     each(__nv_bfloat16{});
@@ -277,6 +278,7 @@ __device__ __forceinline__ void load_apart(const void* p, int32_t dtype, int64_t
   else
     each(float{});
 }
+template <int APART>
 __device__ __forceinline__ bool store_apart(void* p, int32_t dtype, int64_t i, const bool (&in)[4], const float (&v)[4]) {
   bool bad = false;
   auto each = [&](auto type) {
@@ -285,7 +287,7 @@ __device__ __forceinline__ bool store_apart(void* p, int32_t dtype, int64_t i, c
     for (int k = 0; k < 4; ++k)
       if (in[k]) {
         bad |= beyond<T>(v[k]);
-        static_cast<T*>(p)[i + 32 * k] = from_float<T>(v[k]);
+        static_cast<T*>(p)[i + APART * k] = from_float<T>(v[k]);
       }
   };
   if (dtype == OPR_DTYPE_BF16)
@@ -296,16 +298,17 @@ __device__ __forceinline__ bool store_apart(void* p, int32_t dtype, int64_t i, c
     each(float{});
   return bad;
 }
+template <int APART>
 __device__ __forceinline__ bool finish_apart(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, const bool (&in)[4],
                                              float (&v)[4], const float (&bias)[4], const float (&residual)[4]) {
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] += bias[k];
-  if (e.z != nullptr) bad |= store_apart(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, in, v);
+  if (e.z != nullptr) bad |= store_apart<APART>(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, in, v);
   activate_row<4>(v, e.activation);
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] += residual[k];
-  return store_apart(e.y, e.y_dtype, m * e.ldy + n, in, v) || bad;
+  return store_apart<APART>(e.y, e.y_dtype, m * e.ldy + n, in, v) || bad;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -509,25 +512,26 @@ __global__ void __launch_bounds__(kProductThreads, 2)
       bad |= finish_row<4>(a.e, a.f16 != 0, m0 + line, n0 + j, f, bias, residual);
     }
   } else {
-    constexpr int kWarps = kProductThreads / 32, kRuns = (kLine + 127) / 128;  // a warp: 128 entries of a line
-    for (int i = warp + static_cast<int>(rank) * kWarps; i < lines * kRuns; i += static_cast<int>(ranks) * kWarps) {
-      const int line = i / kRuns, j = i % kRuns * 128 + lane;
-      bool in[4];
+    // a line of 128 entries to 32 lanes, one of 64 to 16
+    constexpr int kLanes = kLine / 4, kTeams = kProductThreads / kLanes;
+    const int team = threadIdx.x / kLanes, j = threadIdx.x % kLanes;
+    bool in[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) in[k] = j + 32 * k < len;
-      if (!in[0]) continue;
-      float bias[4] = {}, residual[4] = {}, f[4] = {};
-      if (a.e.bias != nullptr) load_apart(a.e.bias, a.e.bias_dtype, n0 + j, in, bias);
+    for (int k = 0; k < 4; ++k) in[k] = j + kLanes * k < len;
+    float bias[4] = {};
+    if (a.e.bias != nullptr) load_apart<kLanes>(a.e.bias, a.e.bias_dtype, n0 + j, in, bias);
+    for (int line = team + static_cast<int>(rank) * kTeams; line < lines && in[0]; line += static_cast<int>(ranks) * kTeams) {
+      float residual[4] = {}, f[4] = {};
       if (a.e.residual != nullptr)
-        load_apart(a.e.residual, a.e.residual_dtype, (m0 + line) * a.e.ld_residual + n0 + j, in, residual);
+        load_apart<kLanes>(a.e.residual, a.e.residual_dtype, (m0 + line) * a.e.ld_residual + n0 + j, in, residual);
 #pragma unroll
       for (int r = 0; r < kMaxSplit; ++r) {
         if (r >= static_cast<int>(ranks)) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (in[k]) f[k] += load_peer(peer[r] + 4 * (line * kLineLd + j + 32 * k));
+          if (in[k]) f[k] += load_peer(peer[r] + 4 * (line * kLineLd + j + kLanes * k));
       }
-      bad |= finish_apart(a.e, a.f16 != 0, m0 + line, n0 + j, in, f, bias, residual);
+      bad |= finish_apart<kLanes>(a.e, a.f16 != 0, m0 + line, n0 + j, in, f, bias, residual);
     }
   }
   if (bad) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
@@ -1131,13 +1135,32 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // the clusters within its GPCs; as the occupancy query reports them).
 constexpr int kSlots[kMaxSplit] = {296, 296, 279, 284, 280, 270, 259, 264};
 
-// CTAs over which the depth of each tile is split: as many as run at one time, with
-// four slices or more to each.
-int tile_split(int64_t tiles, int64_t slices) {
-  int split = 1;
-  for (int c = 2; c <= kMaxSplit; ++c)
-    if (tiles * c <= kSlots[c - 1] && slices >= 4 * c) split = c;
-  return split;
+// Time (us) of a product in 128 x BN tiles with the depth of each split over the
+// least costly number of CTAs, which comes back in `split`; the 5 us or so that any
+// product takes left out.  As measured over 128 to 16384 rows, 144 to 4096 columns and
+// 64 to 65536 deep:
+//   a 64-deep slice of a CTA that has its SM to itself   0.30 (BN 64)  0.44 (BN 128)
+//   of two that share one, each                          0.44          0.54
+//   joining c parts, each past the first                 0.1 .. 0.6    0.25 .. 1.1
+//   (with the CTAs that read one another's at one time)
+//   the epilogue of each tile of an SM past the first    1.6           2.9
+// Other widths (BN 16) are taken as 64.
+double tile_cost(int64_t tiles, int64_t slices, int bn, int* split) {
+  const bool wide = bn == 128;
+  double best = 0.0;
+  for (int c = 1; c <= kMaxSplit; ++c) {
+    const int64_t ctas = tiles * c;
+    if (c > 1 && (ctas > kSlots[c - 1] || slices < 4 * c)) continue;
+    const double each = static_cast<double>(slices) / c, own = wide ? 0.44 : 0.30, two = wide ? 0.54 : 0.44;
+    double t = ctas <= 148 ? each * own : std::max(each * two, ctas * each / 148 * two / 2);
+    t += (c - 1) * (wide ? 0.25 + ctas / 148.0 * 0.5 : 0.1 + ctas / 148.0 * 0.3);
+    t += static_cast<double>(ceil_div(tiles, 148) - 1) * (wide ? 2.9 : 1.6);
+    if (c == 1 || t < best) {
+      best = t;
+      *split = c;
+    }
+  }
+  return best;
 }
 
 template <bool P_MN, bool Q_MN, int BN, bool SWAP>
@@ -1152,7 +1175,8 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cuda
   if (e != cudaSuccess) return e;
   const int64_t tiles_p = ceil_div(a.rows_p, kRowsP), tiles_q = ceil_div(a.rows_q, BN), tiles = tiles_p * tiles_q;
   const int64_t slices = ceil_div(a.depth, kDepth);
-  const int split = tile_split(tiles, slices);
+  int split = 1;
+  tile_cost(tiles, slices, BN, &split);
   a.vec = rows_aligned(a.e) && (SWAP ? a.rows_p : a.rows_q) % 4 == 0 && reinterpret_cast<uintptr_t>(a.e.bias) % 16 == 0;
   cudaLaunchConfig_t cfg{};
   a.tiles_p = static_cast<int32_t>(tiles_p);
@@ -1190,24 +1214,17 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cuda
   return cudaGetLastError();
 }
 
-// Which kernel: the least of the times (us) that the three shapes of work take, as
-// measured over products of 128 to 16384 rows, 144 to 4096 columns and 128 to 65536
-// deep (a few us of launch, pipeline fill and last epilogue, alike for all, left out):
-//   pairs     0.36 a 256 x 256 slice of 64, whole waves of 74 tiles
-//   tiles     0.27 a 128 x 128 slice or 0.20 a 128 x 64 slice per SM while two CTAs
-//             share it, but at least 0.36 or 0.25 a slice of one CTA's own chain
-// e.g. 777 x 4096 x 4096 (device us): pairs 32, tiles 35 and 47; 512 rows: 31, 24, 27;
-// 128 rows: 30, 17, 15; a weight gradient of 1024 x 1024 over 16384 rows: 88, 38, 48.
+// Which kernel: CTA pairs, 0.36 us a 256 x 256 slice in whole waves of 74 tiles and
+// 3 us more than a single tile for their start and end, or tiles.  E.g. (device us)
+// 777 x 4096 x 4096: pairs 29, tiles of 128 35, of 64 47; 512 rows: 31, 24, 27; 128
+// rows: 30, 16, 15; a weight gradient of 1024 x 1024 over 16384 rows: 88, 38, 48.
 template <bool P_MN, bool Q_MN>
 cudaError_t launch_product(const Operand& p, const Operand& q, const ProductArgs& a, cudaStream_t stream) {
-  const double slices = static_cast<double>(ceil_div(a.depth, kDepth));
-  const double pairs = static_cast<double>(ceil_div(ceil_div(a.rows_p, kPairTile) * ceil_div(a.rows_q, 256), 74)) * slices * 0.36;
-  auto tiles = [&](int bn, double shared, double own) {
-    const int64_t n = ceil_div(a.rows_p, kRowsP) * ceil_div(a.rows_q, bn);
-    const int split = tile_split(n, ceil_div(a.depth, kDepth));
-    return std::max(n * slices / 148 * shared, static_cast<double>(ceil_div(n * split, 296)) * slices / split * own);
-  };
-  const double wide = tiles(128, 0.27, 0.36), narrow = tiles(64, 0.20, 0.25);
+  const int64_t slices = ceil_div(a.depth, kDepth);
+  const double pairs = 0.36 * slices * ceil_div(ceil_div(a.rows_p, kPairTile) * ceil_div(a.rows_q, kPairTile), 148 / 2) + 3.0;
+  int split = 1;
+  const double wide = tile_cost(ceil_div(a.rows_p, kRowsP) * ceil_div(a.rows_q, 128), slices, 128, &split);
+  const double narrow = tile_cost(ceil_div(a.rows_p, kRowsP) * ceil_div(a.rows_q, 64), slices, 64, &split);
   if (pairs <= wide && pairs <= narrow) return launch_pairs<P_MN, Q_MN>(p, q, a, stream);
   if (wide <= narrow) return launch_tiles<P_MN, Q_MN, 128, false>(p, q, a, stream);
   return launch_tiles<P_MN, Q_MN, 64, false>(p, q, a, stream);
