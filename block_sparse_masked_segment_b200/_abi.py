@@ -669,14 +669,18 @@ def _call(name: str, device: torch.device, *args) -> None:
         _check(st, name)
 
 
-def _new(shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
-    """An empty contiguous tensor (empty_strided takes half of torch.empty's time, and a call here
-    allocates up to six)."""
-    strides, step = [], 1
-    for n in reversed(shape):
-        strides.append(step)
-        step *= n
-    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
+# Empty contiguous tensors: empty_strided takes half of torch.empty's time, and a call here
+# allocates up to six.
+def _new1(n: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
+
+
+def _new2(m: int, n: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    return torch.empty_strided((m, n), (n, 1), dtype=dtype, device=device)
+
+
+def _new3(t: int, h: int, d: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    return torch.empty_strided((t, h, d), (h * d, d, 1), dtype=dtype, device=device)
 
 
 def _one_device(call: str, first: torch.Tensor, *ts: torch.Tensor | None) -> None:
@@ -756,7 +760,10 @@ def opr_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k
     if out is None:
         if out_dtype not in _DT:
             raise OprError("out_dtype must be bf16, fp16 or fp32")
-        out = tuple([_new(t.shape, out_dtype, q.device) for t in ins])
+        device, hkv = q.device, k.shape[1]
+        out = (_new3(total, hq, d, out_dtype, device), _new3(total, hkv, d, out_dtype, device))
+        if v is not None:
+            out += (_new3(total, hkv, d, out_dtype, device),)
     else:
         if len(out) != len(ins):
             raise OprError("out must be (q_out, k_out), with v (q_out, k_out, v_out)")
@@ -791,6 +798,7 @@ def opr_qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k:
     hkv = k.shape[1]
     _norm_weights(q, k, q_weight, k_weight)
     _rotation("opr_qk_norm_rope_bwd", q, pos_id, freq, row_map, dev_status)
+    device = q.device
     grads = (dq, dk) if dv is None else (dq, dk, dv)
     shapes = (q.shape, k.shape, k.shape)
     _need_cuda(*grads)
@@ -800,7 +808,9 @@ def opr_qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k:
         out_dtype = q.dtype if out_dtype is None else out_dtype
         if out_dtype not in _DT:
             raise OprError("out_dtype must be bf16, fp16 or fp32")
-        out = tuple([_new(g.shape, out_dtype, q.device) for g in grads])
+        out = (_new3(total, hq, d, out_dtype, device), _new3(total, hkv, d, out_dtype, device))
+        if dv is not None:
+            out += (_new3(total, hkv, d, out_dtype, device),)
         strides = (hq * d, hkv * d, hkv * d)
     else:
         if len(out) != len(grads):
@@ -809,12 +819,12 @@ def opr_qk_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k:
         if any(o.dtype != out[0].dtype for o in out):
             raise OprError("the tensors of out must have one type")
     if workspace is None:
-        workspace = _new((opr_qk_norm_rope_bwd_workspace_bytes(total, hq, hkv, d),), torch.uint8, q.device)
+        workspace = _new1(opr_qk_norm_rope_bwd_workspace_bytes(total, hq, hkv, d), torch.uint8, device)
     else:
         _need_cuda(workspace)
     _one_device("opr_qk_norm_rope_bwd", q, k, q_weight, k_weight, workspace, *grads, *out)
-    dqw, dkw = _new((d,), torch.float32, q.device), _new((d,), torch.float32, q.device)
-    _call("opr_qk_norm_rope_bwd", q.device, _ptr(dq), _ptr(dk), _ptr(dv), _DT[dq.dtype], _ptr(q), qs, _ptr(k), ks,
+    dqw, dkw = _new1(d, torch.float32, device), _new1(d, torch.float32, device)
+    _call("opr_qk_norm_rope_bwd", device, _ptr(dq), _ptr(dk), _ptr(dv), _DT[dq.dtype], _ptr(q), qs, _ptr(k), ks,
           _DT[q.dtype], _ptr(q_weight), _ptr(k_weight), _DT[q_weight.dtype], eps, _ptr(pos_id), _ptr(freq),
           2 * freq.numel(), bool(interleaved), scale, _ptr(row_map), total, hq, hkv, d, _ptr(out[0]), strides[0],
           _ptr(out[1]), strides[1], _ptr(out[2]) if dv is not None else None, strides[2] if dv is not None else 0,
@@ -852,7 +862,7 @@ def _status_word(dev_status, device) -> torch.Tensor:
 def _scratch(workspace, need: int, device):
     """The caller's workspace, or one of `need` bytes (None for 0): (tensor, bytes)."""
     if workspace is None:
-        workspace = _new((need,), torch.uint8, device) if need else None
+        workspace = _new1(need, torch.uint8, device) if need else None
     elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
         raise OprError(f"workspace must be contiguous on {device}")
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -895,9 +905,9 @@ def opr_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
         out_dtype = x.dtype if out_dtype is None else out_dtype
         if out_dtype not in _DT:
             raise OprError("out_dtype must be bf16, fp16 or fp32")
-        out = _new((m, n), out_dtype, x.device)
+        out = _new2(m, n, out_dtype, x.device)
     ldy = _matrix("out", out, shape=(m, n))
-    z = _new((m, n), x.dtype, x.device) if save_z else None
+    z = _new2(m, n, x.dtype, x.device) if save_z else None
     _one_device("opr_linear", x, w, bias, residual, out)
     status = _status_word(dev_status, x.device)
     need = load_library().opr_linear_workspace_bytes(_ptr(x), ldx, _ptr(w), ldw, m, n, k)
@@ -954,11 +964,11 @@ def opr_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.
             return given
         if dtype not in _DT:
             raise OprError("gradients are bf16, fp16 or fp32")
-        return _new(shape, dtype, x.device)
+        return _new2(*shape, dtype, x.device)
 
     dx = result(out[0], need_dx, x.dtype if dx_dtype is None else dx_dtype, (m, k))
     dw = result(out[1], need_dw, w.dtype if dw_dtype is None else dw_dtype, (n, k))
-    db = _new((n,), torch.float32, x.device) if bias else None
+    db = _new1(n, torch.float32, x.device) if bias else None
     ldx_out = 0 if dx is None else _matrix("dx", dx, shape=(m, k))
     ldw_out = 0 if dw is None else _matrix("dw", dw, shape=(n, k))
     _one_device("opr_linear_bwd", x, w, dy, z, dx_residual, dx, dw)
