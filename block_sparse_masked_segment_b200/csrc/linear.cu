@@ -2,7 +2,21 @@
 // and its gradients.
 //   z = x w^T + bias;  y = act(z) + residual
 //   dz = dy act'(z);  db = sum over rows of dz;  dx = dz w;  dw = dz^T x
-// 16-bit operands, fp32 sums, each output rounded once.
+// 16-bit operands, fp32 sums (tcgen05, accumulators in TMEM), each output rounded once.
+//
+// Two kernels: persistent CTA pairs on 256 x 256 tiles, and single tiles of 128 x 128 or
+// 128 x 64 (the weight on the 128 rows where x has few) with the depth of each split
+// over a cluster.  Measured (device us; a library's product of the same sizes in
+// brackets; 1645.8 TFLOP/s is the measured peak):
+//   16384 x 6144 x 4096           535  1.54 PFLOP/s  [546]    at the power limit
+//   dx, dw of 16384 x 4096 x 4096 350, 381           [350, 352]  dw: 3.5 waves of tiles
+//   777 x 4096 x 4096              29  0.91 PFLOP/s           fetches from L2
+//   one row, 6144 x 4096         13.3  3.8 TB/s      [11.9]   latency of start and join
+//   777 x 1000 x 1112            11.6                [6.2]    latency of start and join
+// Tried and slower: the last wave's tiles shared out along the depth over all pairs, the
+// parts joined through L2 (dw 433: pairs at different depths share no rows in L2, and
+// the join adds 15 us); the last tiles in halves of 128 columns (dw 407, with the
+// boxes of 64 rows that takes); tiles of 256 x 128 and 256 x 64.
 #include <algorithm>
 #include <atomic>
 
@@ -262,14 +276,16 @@ __device__ __forceinline__ void load_residual(const LinearEpilogue& e, int64_t m
   if (e.residual != nullptr) load_row<W>(e.residual, e.residual_dtype, m * e.ld_residual + n, v);
 }
 
-// Four entries of row m, APART from one to the next (neighbouring lanes take neighbouring
-// ones), those of `in` only: any alignment.  The loads go out together.
-template <int APART>
-__device__ __forceinline__ void load_apart(const void* p, int32_t dtype, int64_t i, const bool (&in)[4], float (&v)[4]) {
+// W entries, `step` from one to the next (along a row, or down a column: neighbouring
+// lanes take neighbouring columns), those of `in` only: any alignment.  The loads go
+// out together.
+template <int W>
+__device__ __forceinline__ void load_apart(const void* p, int32_t dtype, int64_t i, int64_t step, const bool (&in)[W],
+                                           float (&v)[W]) {
   auto each = [&](auto type) {
     using T = decltype(type);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = in[k] ? as_float(static_cast<const T*>(p)[i + APART * k]) : 0.f;
+    for (int k = 0; k < W; ++k) v[k] = in[k] ? as_float(static_cast<const T*>(p)[i + k * step]) : 0.f;
   };
   if (dtype == OPR_DTYPE_BF16)
     each(__nv_bfloat16{});
@@ -278,16 +294,17 @@ __device__ __forceinline__ void load_apart(const void* p, int32_t dtype, int64_t
   else
     each(float{});
 }
-template <int APART>
-__device__ __forceinline__ bool store_apart(void* p, int32_t dtype, int64_t i, const bool (&in)[4], const float (&v)[4]) {
+template <int W>
+__device__ __forceinline__ bool store_apart(void* p, int32_t dtype, int64_t i, int64_t step, const bool (&in)[W],
+                                            const float (&v)[W]) {
   bool bad = false;
   auto each = [&](auto type) {
     using T = decltype(type);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < W; ++k)
       if (in[k]) {
         bad |= beyond<T>(v[k]);
-        static_cast<T*>(p)[i + APART * k] = from_float<T>(v[k]);
+        static_cast<T*>(p)[i + k * step] = from_float<T>(v[k]);
       }
   };
   if (dtype == OPR_DTYPE_BF16)
@@ -298,17 +315,22 @@ __device__ __forceinline__ bool store_apart(void* p, int32_t dtype, int64_t i, c
     each(float{});
   return bad;
 }
-template <int APART>
-__device__ __forceinline__ bool finish_apart(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, const bool (&in)[4],
-                                             float (&v)[4], const float (&bias)[4], const float (&residual)[4]) {
+// Outputs from (m, n) on, `cols` columns or, where that is 0, one row apart.
+template <int W>
+__device__ __forceinline__ bool finish_apart(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, int cols,
+                                             const bool (&in)[W], float (&v)[W], const float (&bias)[W]) {
   bool bad = false;
+  float residual[W] = {};
+  if (e.residual != nullptr)
+    load_apart<W>(e.residual, e.residual_dtype, m * e.ld_residual + n, cols ? cols : e.ld_residual, in, residual);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] += bias[k];
-  if (e.z != nullptr) bad |= store_apart<APART>(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, in, v);
-  activate_row<4>(v, e.activation);
+  for (int k = 0; k < W; ++k) v[k] += bias[k];
+  if (e.z != nullptr)
+    bad |= store_apart<W>(e.z, f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, m * e.ldz + n, cols ? cols : e.ldz, in, v);
+  activate_row<W>(v, e.activation);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] += residual[k];
-  return store_apart<APART>(e.y, e.y_dtype, m * e.ldy + n, in, v) || bad;
+  for (int k = 0; k < W; ++k) v[k] += residual[k];
+  return store_apart<W>(e.y, e.y_dtype, m * e.ldy + n, cols ? cols : e.ldy, in, v) || bad;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -519,11 +541,9 @@ __global__ void __launch_bounds__(kProductThreads, 2)
 #pragma unroll
     for (int k = 0; k < 4; ++k) in[k] = j + kLanes * k < len;
     float bias[4] = {};
-    if (a.e.bias != nullptr) load_apart<kLanes>(a.e.bias, a.e.bias_dtype, n0 + j, in, bias);
+    if (a.e.bias != nullptr) load_apart<4>(a.e.bias, a.e.bias_dtype, n0 + j, kLanes, in, bias);
     for (int line = team + static_cast<int>(rank) * kTeams; line < lines && in[0]; line += static_cast<int>(ranks) * kTeams) {
-      float residual[4] = {}, f[4] = {};
-      if (a.e.residual != nullptr)
-        load_apart<kLanes>(a.e.residual, a.e.residual_dtype, (m0 + line) * a.e.ld_residual + n0 + j, in, residual);
+      float f[4] = {};
 #pragma unroll
       for (int r = 0; r < kMaxSplit; ++r) {
         if (r >= static_cast<int>(ranks)) break;
@@ -531,7 +551,7 @@ __global__ void __launch_bounds__(kProductThreads, 2)
         for (int k = 0; k < 4; ++k)
           if (in[k]) f[k] += load_peer(peer[r] + 4 * (line * kLineLd + j + kLanes * k));
       }
-      bad |= finish_apart<kLanes>(a.e, a.f16 != 0, m0 + line, n0 + j, in, f, bias, residual);
+      bad |= finish_apart<4>(a.e, a.f16 != 0, m0 + line, n0 + j, kLanes, in, f, bias);
     }
   }
   if (bad) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
@@ -631,6 +651,28 @@ __device__ __forceinline__ void stage_row32(uint8_t* block, int row, const float
   for (int g = 0; g < 8; ++g)
     *reinterpret_cast<float4*>(block + row * 128 + ((g ^ row) & 7) * 16) =
         make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+}
+
+// Finishes a lane's column of a block staged by stage_row32, eight rows at a time.  A
+// call of its own: its code would slow the epilogue that it stands in.
+__device__ __noinline__ bool finish_column(const LinearEpilogue& e, bool f16, int64_t m, int64_t n, int rows,
+                                           const uint8_t* block, int lane, float bias) {
+  bool bad = false;
+  float b8[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) b8[k] = bias;
+#pragma unroll 1
+  for (int row = 0; row < rows; row += 8) {
+    bool in[8];
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      in[k] = row + k < rows;
+      f[k] = *reinterpret_cast<const float*>(block + (row + k) * 128 + (((lane >> 2) ^ (row + k)) & 7) * 16 + (lane & 3) * 4);
+    }
+    bad |= finish_apart<8>(e, f16, m + row, n, 0, in, f, b8);
+  }
+  return bad;
 }
 
 // A lane's row of a residual block, as loaded; columns past the end (a multiple of
@@ -860,13 +902,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
           stage_row32(stage, lane, v);
           __syncwarp();
           const int rows = a.rows_p - m0 < 32 ? static_cast<int>(a.rows_p - m0) : 32;
-          if (n0 + lane < a.rows_q) {
-#pragma unroll 1
-            for (int row = 0; row < rows; ++row) {
-              const uint8_t* at = stage + row * 128 + (((lane >> 2) ^ row) & 7) * 16 + (lane & 3) * 4;
-              bad |= finish(e, f16, m0 + row, n0 + lane, *reinterpret_cast<const float*>(at));
-            }
-          }
+          if (n0 + lane < a.rows_q)
+            bad |= finish_column(e, f16, m0, n0 + lane, rows, stage, lane, e.bias != nullptr ? bias[32 * c + lane] : 0.f);
           continue;
         }
         if (e.bias != nullptr) {
@@ -985,7 +1022,8 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
 // rows, taken before dz is rounded.  A thread takes W neighbouring columns (eight
 // where the rows allow 16-byte accesses, else one); the block's 256 threads are `wide`
 // column groups times 256 / wide rows, whose sums are added in order at the end.
-// HBM-bound: dy and z are read once, dz written once.
+// HBM-bound: dy and z are read once, dz written once (2377 x 4096 with SiLU and db: 14.5
+// us for 58 MB, 4.0 TB/s, 3 us of it the column sums' second kernel).
 constexpr int kDzThreads = 256;
 constexpr int kDzSpan = 32;      // column groups of a block
 constexpr int kDzMaxBlocks = 512;  // row blocks, which sizes the partial sums

@@ -8,8 +8,19 @@
 //   rotation  y_a = s (a cos - b sin),  y_b = s (b cos + a sin)
 //   gradient  g = R^T dy;  xh = h rs;  dw = sum g xh;  u = g w;
 //             dh = rs (u - xh mean(u xh))
-// All arithmetic in fp32, each output rounded once.  HBM-bound: every element is
-// read and written once.
+// All arithmetic in fp32, each output rounded once.
+//
+// Every element is read and written once, so HBM bounds them; next to it the issue of
+// instructions (16 entries a lane: the packed arithmetic, the tables and the fast
+// quotients are there for that).  Measured (device time; a plain copy of as many bytes
+// in brackets):
+//   16384 tokens x 32 heads of 128, half of each rotated, bf16 to fp16   50 us, 5.4 TB/s
+//   32749 tokens x 8 heads of 128, fp32, interleaved                     46 us, 5.8 TB/s
+//   16384 tokens, 32q/8kv heads of 128 and v, norm                       80 us, 5.0 TB/s [71 us]
+//   65536 tokens, 64q/8kv heads of 128 and v, fp32 gradients            838 us, 6.2 TB/s [824 us]
+// Tried and slower: persistent blocks that make the next tile's tables between rounds
+// (norm 117 us), rows brought by bulk copies to a ring in shared memory (104 us), more
+// blocks an SM with fewer registers (five 92 us, six 110 us).
 #include <algorithm>
 
 #include "layer.cuh"
@@ -49,7 +60,9 @@ __device__ __forceinline__ void pair_of(const HeadArgs& a, int j, int& ia, int& 
   ib = a.interleaved ? 2 * j + 1 : j + a.pairs;
 }
 
-// One warp per (token, head), entry by entry: any head_dim, stride and alignment.
+// One warp per (token, head), entry by entry: any head_dim, stride and alignment.  What
+// the vector form below does not take (odd sizes and strides), at a third to a fifth of
+// its speed.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(32 * kWarps) heads_kernel(const HeadArgs a, int32_t heads_total) {
   const int lane = threadIdx.x & 31;
