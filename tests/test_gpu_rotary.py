@@ -34,7 +34,7 @@ def rotary_bound(x, rot, interleaved, scale):
 # total, heads, d, rot: one token, odd counts, pairs off the grid of eight, whole and part of the head
 SHAPES = [(1, 1, 64, 64), (1, 32, 128, 128), (3, 2, 128, 64), (37, 5, 80, 20), (129, 3, 256, 256), (65, 1, 96, 48),
           (17, 7, 6, 2), (260, 8, 128, 32), (33, 2, 72, 64), (40, 2, 200, 16),
-          (700, 3, 80, 80), (450, 1, 48, 16), (300, 40, 128, 128)]
+          (700, 3, 80, 80), (450, 1, 48, 16), (300, 40, 128, 128), (50, 3, 16, 16), (33, 2, 32, 16)]
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
@@ -179,7 +179,7 @@ def weights(rng, d, dtype):
 
 QK_SHAPES = [(1, 1, 1, 64, 64), (1, 32, 8, 128, 128), (5, 3, 1, 128, 64), (67, 8, 2, 64, 32), (130, 4, 4, 256, 256),
              (19, 2, 1, 80, 20), (300, 5, 1, 128, 128), (12, 2, 2, 6, 4), (21, 3, 3, 72, 64), (40, 1, 1, 200, 16),
-             (700, 2, 1, 80, 80), (450, 1, 1, 48, 16), (310, 20, 2, 128, 96), (900, 1, 5, 256, 64)]
+             (700, 2, 1, 80, 80), (450, 1, 1, 48, 16), (310, 20, 2, 128, 96), (900, 1, 5, 256, 64), (50, 3, 1, 16, 16), (33, 2, 2, 32, 16)]
 
 
 @pytest.mark.parametrize("packed", [False, True])
@@ -320,6 +320,53 @@ def test_qk_norm_gradient_of_many_rows():
     for got, dy in ((gq, dq), (gk, dk)):
         ref = lo.rotate(to64(dy), to64(pos), to64(freq), inverse=True) / np.sqrt(1 + EPS)
         within(got, ref.sum((0, 1)), np.abs(ref).sum((0, 1)) * 2.0 ** -14, "fp32")
+
+
+def test_qk_norm_gradient_of_many_tokens_of_one_wide_head():
+    """The largest tables that a block holds: 32 tokens of 128 pairs.  Closed form as above."""
+    total, d = 9700, 256
+    rng = np.random.default_rng(24)
+    dq, dk = heads(rng, total, 1, d, "fp32"), heads(rng, total, 1, d, "fp32")
+    one, w = torch.ones(total, 1, d, device="cuda"), torch.ones(d, device="cuda")
+    pos = positions(rng, total)
+    freq, _ = opr.opr_rotary_frequencies(d, 1e4)
+    *_, gq, gk = opr.opr_qk_norm_rope_bwd(dq, dk, one, one, w, w, pos, freq, EPS)
+    for got, dy in ((gq, dq), (gk, dk)):
+        ref = lo.rotate(to64(dy), to64(pos), to64(freq), inverse=True) / np.sqrt(1 + EPS)
+        within(got, ref.sum((0, 1)), np.abs(ref).sum((0, 1)) * 2.0 ** -14, "fp32")
+
+
+def test_rows_past_two_to_the_31_entries():
+    """More than 2^31 entries in one tensor: the last tokens of the rotation, of the norm (in place) and of
+    its gradient (one projection's packed rows)."""
+    total, hq, hkv, d = 140000, 104, 8, 128
+    x = torch.zeros(total, hq + 2 * hkv, d, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(3)
+    tail = slice(total - 3, total)
+    x[tail] = torch.randn(3, hq + 2 * hkv, d, device="cuda", generator=g).bfloat16()
+    keep = x[tail].clone()
+    pos = torch.arange(total, dtype=torch.int32, device="cuda")
+    freq, _ = opr.opr_rotary_frequencies(d, 1e6)
+    w = (1 + 0.1 * torch.randn(d, device="cuda", generator=g)).bfloat16()
+    y = opr.opr_rotary(x, pos, freq, out=torch.empty_like(x))
+    K = to64(keep)
+    P, F, W = to64(pos[tail]), to64(freq), to64(w)
+    within(y[tail], lo.rotate(K, P, F), rotary_bound(K, d, False, 1.0), "bf16")
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    dq, dk, dv = (torch.zeros(total, h, d, dtype=torch.bfloat16, device="cuda") for h in (hq, hkv, hkv))
+    for t in (dq, dk, dv):
+        t[tail] = torch.randn(3, t.shape[1], d, device="cuda", generator=g).bfloat16()
+    out = (y[:, :hq], y[:, hq:hq + hkv], y[:, hq + hkv:])
+    y[:-3] = 0
+    *_, gqw, _ = opr.opr_qk_norm_rope_bwd(dq, dk, q, k, w, w, pos, freq, EPS, dv=dv, out=out)
+    for got, dy, a in ((out[0], dq, K[:, :hq]), (out[1], dk, K[:, hq:hq + hkv])):
+        rx, rw = lo.norm_rotate_bwd(to64(dy[tail]), a, W, P, F, EPS)
+        bx, bw = grad_bounds(to64(dy[tail]), a, W, P, F, False, 1.0)
+        within(got[tail], rx, bx, "bf16")
+        if dy is dq:
+            within(gqw, rw, bw, "fp32")
+    assert torch.equal(out[2][tail], dv[tail]) and not y[:-3].any()
 
 
 def test_qk_norm_gradient_of_no_tokens_is_zero():
