@@ -910,7 +910,9 @@ def opr_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
     z = _new2(m, n, x.dtype, x.device) if save_z else None
     _one_device("opr_linear", x, w, bias, residual, out)
     status = _status_word(dev_status, x.device)
-    need = load_library().opr_linear_workspace_bytes(_ptr(x), ldx, _ptr(w), ldw, m, n, k)
+    # none where all rows start on 16-byte boundaries, so that the usual call need not ask
+    need = 0 if not (x.data_ptr() | w.data_ptr() | 2 * ldx | 2 * ldw) & 15 else \
+        load_library().opr_linear_workspace_bytes(_ptr(x), ldx, _ptr(w), ldw, m, n, k)
     workspace, ws_bytes = _scratch(workspace, need, x.device)
     _call("opr_linear", x.device, _ptr(x), ldx, _ptr(w), ldw, _DT[x.dtype], _ptr(bias),
           0 if bias is None else _DT[bias.dtype], ACTIVATIONS[activation], _ptr(residual), ldr,

@@ -10,9 +10,9 @@
 // brackets; 1645.8 TFLOP/s is the measured peak):
 //   16384 x 6144 x 4096           535  1.54 PFLOP/s  [546]    at the power limit
 //   dx, dw of 16384 x 4096 x 4096 350, 381           [350, 352]  dw: 3.5 waves of tiles
-//   777 x 4096 x 4096              29  0.91 PFLOP/s           fetches from L2
-//   one row, 6144 x 4096         13.3  3.8 TB/s      [11.9]   latency of start and join
-//   777 x 1000 x 1112            11.6                [6.2]    latency of start and join
+//   777 x 4096 x 4096              28  0.92 PFLOP/s           fetches from L2
+//   one row, 6144 x 4096         12.3  4.1 TB/s      [11.9]   latency of start and join
+//   777 x 1000 x 1112            10.2                [6.2]    latency of start and join
 // Tried and slower: the last wave's tiles shared out along the depth over all pairs, the
 // parts joined through L2 (dw 433: pairs at different depths share no rows in L2, and
 // the join adds 15 us); the last tiles in halves of 128 columns (dw 407, with the
@@ -433,6 +433,7 @@ __global__ void __launch_bounds__(kProductThreads, 2)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
+  wait_for_previous();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -765,6 +766,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
+  wait_for_previous();
 
   auto fill = [&](int j, int tp, int tq, int slice) {
     const int s = j % kStages;
@@ -982,6 +984,7 @@ struct PackArgs {
   int32_t cols[2];
 };
 __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < a.rows[0] + a.rows[1]; r += warps) {
@@ -1041,6 +1044,7 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const T* dy, int6
   const int64_t r1 = r0 + rows_per_block < m ? r0 + rows_per_block : m;
   float sum[W] = {};
   bool bad = false;
+  wait_for_previous();
   if (j < n) {
 #pragma unroll 2
     for (int64_t i = r0 + row; i < r1; i += kRows) {
@@ -1098,6 +1102,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, i
   const int col = threadIdx.x & 31, part = threadIdx.x >> 5;
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + col;
   double t = 0.0;
+  wait_for_previous();
   if (j < n)
 #pragma unroll 8
     for (int b = part; b < blocks; b += 8) t += partial[static_cast<int64_t>(b) * n + j];
@@ -1216,18 +1221,9 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, ProductArgs a, cuda
   int split = 1;
   tile_cost(tiles, slices, BN, &split);
   a.vec = rows_aligned(a.e) && (SWAP ? a.rows_p : a.rows_q) % 4 == 0 && reinterpret_cast<uintptr_t>(a.e.bias) % 16 == 0;
-  cudaLaunchConfig_t cfg{};
   a.tiles_p = static_cast<int32_t>(tiles_p);
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
-  cfg.blockDim = dim3(kProductThreads);
-  cfg.dynamicSmemBytes = kTileSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mp, mq, a);
+  return launch_overlapped(kernel, dim3(static_cast<unsigned>(tiles * split)), kProductThreads, kTileSmem, split, stream,
+                           mp, mq, a);
 }
 
 template <bool P_MN, bool Q_MN>
@@ -1248,8 +1244,8 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, ProductArgs a, cuda
                 (a.e.z != nullptr && !block_map(&mz, a.e.z, a.e.ldz, a.f16 ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16, a.rows_p, a.rows_q))))
     return cudaErrorInvalidValue;
   const int64_t pairs = std::min<int64_t>(static_cast<int64_t>(a.tiles_p) * a.tiles_q, 148 / 2);
-  kernel<<<static_cast<unsigned>(2 * pairs), kProductThreads, kProductSmem, stream>>>(mp, mq, my, mz, a);
-  return cudaGetLastError();
+  return launch_overlapped(kernel, dim3(static_cast<unsigned>(2 * pairs)), kProductThreads, kProductSmem, 0, stream, mp, mq,
+                           my, mz, a);
 }
 
 // Which kernel: CTA pairs, 0.36 us a 256 x 256 slice in whole waves of 74 tiles and
@@ -1314,8 +1310,8 @@ cudaError_t launch_pack(const PackJob (&jobs)[2], cudaStream_t stream) {
   }
   const int64_t rows = a.rows[0] + a.rows[1];
   if (rows == 0) return cudaSuccess;
-  pack_kernel<<<static_cast<unsigned>(std::min<int64_t>(ceil_div(rows, 8), 148 * 8)), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(pack_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(rows, 8), 148 * 8))), 256, 0,
+                           0, stream, a);
 }
 
 namespace {
@@ -1351,10 +1347,9 @@ cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int64
     float* part = db != nullptr ? partial : nullptr;
     auto go = [&](auto type, auto width) {
       using T = decltype(type);
-      linear_dz_kernel<T, decltype(width)::value><<<grid, kDzThreads, 0, stream>>>(
-          static_cast<const T*>(dy), ld_dy, static_cast<const T*>(z), ldz, m, n, activation, static_cast<T*>(dz), ld_dz,
-          part, plan.rows_per_block, dev_status);
-      return cudaGetLastError();
+      return launch_overlapped(linear_dz_kernel<T, decltype(width)::value>, grid, kDzThreads, 0, 0, stream,
+                               static_cast<const T*>(dy), ld_dy, static_cast<const T*>(z), ldz, m, n, activation,
+                               static_cast<T*>(dz), ld_dz, part, plan.rows_per_block, dev_status);
     };
     auto typed = [&](auto width) {
       return dtype == OPR_DTYPE_BF16 ? go(__nv_bfloat16{}, width) : go(__half{}, width);
@@ -1363,8 +1358,8 @@ cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int64
     if (e != cudaSuccess) return e;
   }
   if (db == nullptr) return cudaSuccess;
-  column_sum_kernel<<<static_cast<unsigned>(ceil_div(n, 32)), 256, 0, stream>>>(partial, plan.rows, n, db);
-  return cudaGetLastError();
+  return launch_overlapped(column_sum_kernel, dim3(static_cast<unsigned>(ceil_div(n, 32))), 256, 0, 0, stream, partial,
+                           plan.rows, n, db);
 }
 
 }  // namespace opr

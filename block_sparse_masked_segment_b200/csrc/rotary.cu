@@ -65,6 +65,7 @@ __device__ __forceinline__ void pair_of(const HeadArgs& a, int j, int& ia, int& 
 // its speed.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(32 * kWarps) heads_kernel(const HeadArgs a, int32_t heads_total) {
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (item >= a.total * heads_total) return;
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(kThreadsVec, 4) heads_vec_kernel(const HeadArg
     if (valid)
       raw = load_unit(static_cast<const TI*>(s.x) + (tok0 + t) * s.x_stride + static_cast<int64_t>(h) * a.d, at);
   };
+  wait_for_previous();
   fetch();  // in flight while the tables are made
   fill_turns<VW>(a, quot.pairs, tok0, ntok, a.inverse != 0, cs);
   bool lost = false;
@@ -705,10 +707,10 @@ cudaError_t launch_heads_vec(const HeadArgs& a, int32_t x_dtype, int32_t y_dtype
         using TO = decltype(to);
         constexpr int VW = vector_width<TI, TO>;
         if (a.set[0].mode == kHeadNormRotate)
-          heads_vec_kernel<TI, TO, VW, G, true><<<blocks, kThreadsVec, smem, stream>>>(a, q, tokens);
-        else
-          heads_vec_kernel<TI, TO, VW, G, false><<<blocks, kThreadsVec, smem, stream>>>(a, q, tokens);
-        return cudaGetLastError();
+          return launch_overlapped(heads_vec_kernel<TI, TO, VW, G, true>, dim3(blocks), kThreadsVec, smem, 0, stream, a, q,
+                                   tokens);
+        return launch_overlapped(heads_vec_kernel<TI, TO, VW, G, false>, dim3(blocks), kThreadsVec, smem, 0, stream, a, q,
+                                 tokens);
       });
     });
   });
@@ -724,8 +726,8 @@ cudaError_t launch_heads(const HeadArgs& a, int32_t x_dtype, int32_t y_dtype, cu
   const int64_t blocks = (a.total * heads + kWarps - 1) / kWarps;
   return with_type(x_dtype, [&](auto ti) {
     return with_type(y_dtype, [&](auto to) {
-      heads_kernel<decltype(ti), decltype(to)><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, stream>>>(a, heads);
-      return cudaGetLastError();
+      return launch_overlapped(heads_kernel<decltype(ti), decltype(to)>, dim3(static_cast<unsigned>(blocks)), 32 * kWarps, 0,
+                               0, stream, a, heads);
     });
   });
 }
@@ -777,6 +779,7 @@ cudaError_t launch_head_grads_vec(const HeadArgs& a, int32_t x_dtype, int32_t dy
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
             if (e != cudaSuccess) return e;
           }
+          // not overlapped with its neighbours: 64K tokens took 837 us so, 850 otherwise
           kernel<<<deal.first[3], kThreadsVec, smem, stream>>>(a, deal, q);
           return cudaGetLastError();
         });

@@ -278,6 +278,25 @@ def test_linear_of_no_rows(n, k):
         assert dx.shape == (0, k) and (dw == 0).all() and (db == 0).all() and dw.shape == (n, k)
 
 
+@pytest.mark.parametrize("m,n", [(5, 128), (64, 72), (33, 65), (300, 320), (16384, 256)])
+def test_each_product_sees_the_one_before(m, n):
+    """A chain of products with a permutation matrix, each on the last one's result, in buffers that take
+    turns: exact, so that any product that started on unfinished rows shows."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    perm = torch.randperm(n, device="cuda", generator=g)
+    w = torch.zeros(n, n, dtype=torch.bfloat16, device="cuda")
+    w[torch.arange(n, device="cuda"), perm] = 1  # (x w^T)[:, j] = x[:, perm[j]]
+    x = torch.randn(m, n, device="cuda", generator=g).bfloat16()
+    want, st = x, status()
+    bufs = [x.clone(), torch.empty_like(x)]
+    torch.cuda.synchronize()
+    for i in range(60):
+        opr.opr_linear(bufs[i % 2], w, out=bufs[1 - i % 2], dev_status=st)
+    for i in range(60):  # and back, through the gradient of x
+        opr.opr_linear_bwd(bufs[i % 2], bufs[i % 2], w, need_dw=False, out=(bufs[1 - i % 2], None), dev_status=st)
+    assert torch.equal(bufs[0], want) and opr.read_status(st) == []
+
+
 def test_linear_refusals_of_tensors():
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
     for bad in (dict(x=x.float()), dict(w=w.half()), dict(w=w[:, :32]), dict(x=x.t()), dict(bias=x[0]),
