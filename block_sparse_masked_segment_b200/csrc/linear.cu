@@ -11,7 +11,7 @@
 //   16384 x 6144 x 4096           535  1.54 PFLOP/s  [546]    at the power limit
 //   dx, dw of 16384 x 4096 x 4096 350, 381           [350, 352]  dw: 3.5 waves of tiles
 //   777 x 4096 x 4096              28  0.92 PFLOP/s           fetches from L2
-//   one row, 6144 x 4096         12.4  4.0 TB/s      [11.9]   latency of start and join
+//   one row, 6144 x 4096         12.3  4.1 TB/s      [11.9]   latency of start and join
 //   777 x 1000 x 1112            10.2                [6.2]    latency of start and join
 // Tried and slower: the last wave's tiles shared out along the depth over all pairs, the
 // parts joined through L2 (dw 433: pairs at different depths share no rows in L2, and
@@ -976,8 +976,8 @@ __global__ void __launch_bounds__(256) no_depth_kernel(const __grid_constant__ P
 
 // Matrices whose rows start off the 16-byte grid, copied to rows that start on it: a
 // warp a row at a time, in 16-byte pieces of the copy, each shifted together from the
-// two 16-byte pieces of the row that it lies across.  Latency bound at the sizes it is
-// met with (1780 rows of 1111: 6 us for 8 MB; single entries instead of pieces took 6.7).
+// two 16-byte pieces of the row that it lies across.  Far below the memory's rate at
+// the sizes it is met with (1780 rows of 1111: 6 us for 8 MB, by itself, caches cold).
 struct PackArgs {
   const uint16_t* x[2];
   uint16_t* y[2];
@@ -1027,7 +1027,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
 // where the rows allow 16-byte accesses, else one); the block's 256 threads are `wide`
 // column groups times 256 / wide rows, whose sums are added in order at the end.
 // HBM-bound: dy and z are read once, dz written once (2377 x 4096 with SiLU and db: 13.3
-// us for 58 MB, 4.4 TB/s, 2 us of it the column sums' second kernel).
+// us for 58 MB, 4.4 TB/s, with the column sums' second kernel).
 constexpr int kDzThreads = 256;
 constexpr int kDzSpan = 32;      // column groups of a block
 constexpr int kDzMaxBlocks = 512;  // row blocks, which sizes the partial sums
@@ -1097,7 +1097,8 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const T* dy, int6
 }
 
 // Sums of the row blocks' partials, 32 columns a block, eight threads to a column,
-// added in a fixed order in fp64.  A few trips to L2 (37 blocks of 4096 columns: 5 us).
+// added in a fixed order in fp64.  37 partials of 4096 columns: 5 us by
+// itself, caches cold.
 __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, int32_t blocks, int32_t n, float* out) {
   __shared__ double sums[8][33];
   const int col = threadIdx.x & 31, part = threadIdx.x >> 5;

@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(32 * kWarps) head_grads_kernel(const HeadArgs 
 }
 
 // dw of set blockIdx.y, 32 entries a block: the blocks' partial sums, 32 threads to
-// an entry, added in a fixed order in fp64.  Trips to L2: 6 us for 296 blocks, 13 us for
-// 2368 (of the 838 us that 64K tokens take).
+// an entry, added in a fixed order in fp64.  By itself, caches cold: 6 us
+// after a first kernel of 295 blocks (2377 tokens), 13 us after one of 2368 (64K tokens).
 __global__ void __launch_bounds__(1024) head_grad_sum_kernel(const HeadArgs a, int32_t blocks_q, int32_t blocks_k) {
   __shared__ double sums[32][33];
   const HeadSet& s = a.set[blockIdx.y];
