@@ -995,14 +995,16 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
     uint16_t* y = one ? a.y[0] + row * a.ldy[0] : a.y[1] + row * a.ldy[1];
     const int cols = one ? a.cols[0] : a.cols[1];
     // bytes that the row starts behind the grid, alike for all lanes
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x) & 15u);
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15u);
     const uint4* grid = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x) - off);
-    const int bytes = 2 * cols;
+    // c: entry of the row that a piece of the copy begins with (a count of bytes would
+    // pass 32 bits in the longest rows)
 #pragma unroll 2
-    for (int c = 16 * lane; c < bytes; c += 512) {
+    for (int64_t c = 8 * lane; c < cols; c += 256) {
+      const int64_t left = cols - c;
       // pieces that hold a byte of the row (a piece never leaves the row's allocation)
-      const uint4 a0 = grid[c / 16];
-      const uint4 a1 = off != 0 && c + 16 - static_cast<int>(off) < bytes ? grid[c / 16 + 1] : make_uint4(0, 0, 0, 0);
+      const uint4 a0 = grid[c / 8];
+      const uint4 a1 = off != 0 && 16 - off < 2 * left ? grid[c / 8 + 1] : make_uint4(0, 0, 0, 0);
       const uint32_t w[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
       uint32_t v[4];
 #pragma unroll
@@ -1011,13 +1013,12 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
         if (off >= 4) lo = w[k + 1], hi = w[k + 2];
         if (off >= 8) lo = w[k + 2], hi = w[k + 3];
         if (off >= 12) lo = w[k + 3], hi = k < 3 ? w[k + 4] : w[7];
-        v[k] = (off & 2u) != 0 ? __funnelshift_r(lo, hi, 16) : lo;
+        v[k] = (off & 2) != 0 ? __funnelshift_r(lo, hi, 16) : lo;
       }
-      const int left = bytes - c;  // zeros behind the row
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (left < 4 * k + 4) v[k] = left > 4 * k ? v[k] & 0xFFFFu : 0u;
-      *reinterpret_cast<uint4*>(y + c / 2) = make_uint4(v[0], v[1], v[2], v[3]);
+      for (int k = 0; k < 4; ++k)  // zeros behind the row
+        if (left < 2 * k + 2) v[k] = left > 2 * k ? v[k] & 0xFFFFu : 0u;
+      *reinterpret_cast<uint4*>(y + c) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
 }

@@ -405,3 +405,18 @@ def test_linear_reports_a_pipeline_timeout(sizes):
         lib.opr_testing_set_wait_limit_ns(prev)
     assert opr.read_status(st) == [_abi.DEV_BITS[8]]
     assert torch.equal(opr.opr_linear(x, w, dev_status=st.zero_()), want) and opr.read_status(st) == []
+
+
+@pytest.mark.parametrize("k", [2 ** 30 - 7, 2 ** 30 + 9])
+def test_linear_copies_rows_whose_bytes_pass_32_bits(k):
+    """One row each of x and w off the 16-byte grid, about 2^31 bytes long: every piece of them reaches the
+    copies (the workspace is NaN before).  Ones in a few places, so the sum is exact."""
+    at = [0, 7, 2 ** 29 - 1, 2 ** 29, 2 ** 29 + 300, k - 513, k - 256, k - 9, k - 8, k - 2, k - 1]
+    x = torch.zeros(k + 1, dtype=torch.bfloat16, device="cuda")[1:].view(1, k)
+    w = torch.zeros(k + 3, dtype=torch.bfloat16, device="cuda")[3:].view(1, k)
+    x[0, at], w[0, at] = 1, 1
+    x[0, [1, 2 ** 29 + 1, k - 3]] = 1  # against zeros of w
+    ws = torch.full((opr.opr_linear_workspace_bytes(x, w) // 4,), float("nan"), device="cuda")
+    st = status()
+    y = opr.opr_linear(x, w, out_dtype=torch.float32, workspace=ws, dev_status=st)
+    assert opr.read_status(st) == [] and y.item() == len(at)
