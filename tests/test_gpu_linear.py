@@ -420,3 +420,33 @@ def test_linear_copies_rows_whose_bytes_pass_32_bits(k):
     st = status()
     y = opr.opr_linear(x, w, out_dtype=torch.float32, workspace=ws, dev_status=st)
     assert opr.read_status(st) == [] and y.item() == len(at)
+
+
+@pytest.mark.parametrize("activation", ["silu", "gelu", "gelu_tanh"])
+def test_activations_of_every_bf16_exponent(activation):
+    """z from the smallest normal bf16 to the largest, both signs, as above; the slope at the infinities is
+    its limit, 0 or 1, and NaN stays NaN.  (In fp64 the formulas reach these limits without overflow.)"""
+    e = np.arange(-126, 128)
+    z = np.concatenate([s * m * 2.0 ** e for s in (1, -1) for m in (1, 1.25, 1.5, 1.75)])
+    z = torch.from_numpy(z).to("cuda", torch.bfloat16)
+    one = torch.zeros(8, 8, dtype=torch.bfloat16, device="cuda")
+    one[0, 0] = 1
+    x = torch.zeros(len(z), 8, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = z
+    y = opr.opr_linear(x, one, activation=activation, out_dtype=torch.float32)[:, 0]
+    Z = to64(z)
+    with np.errstate(over="ignore"):
+        ref, slope = lo.act(Z, activation), lo.act_slope(Z, activation)
+    within(y, ref, (np.abs(Z) + 1) * 2.0 ** -20 * np.where(np.abs(Z) > 64, 0.25, 1), "fp32")
+    z = torch.cat((z, torch.tensor([float("inf"), float("-inf"), float("nan")], device="cuda").bfloat16()))
+    slope = np.concatenate((slope, [1, 0]))
+    for n in (1, 8):  # entry by entry, and in 16-byte accesses
+        dy, zn = torch.ones(len(z), n, dtype=torch.bfloat16, device="cuda"), z[:, None].expand(-1, n).contiguous()
+        w = torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+        w[n - 1] = 1
+        x = torch.zeros(len(z), 8, dtype=torch.bfloat16, device="cuda")
+        dz, _, db = opr.opr_linear_bwd(dy, x, w, zn, activation, need_dw=False, bias=True, dx_dtype=torch.float32)
+        within(dz[:-1, 0], slope, 2.0 ** -19 + half_step("bf16") * np.abs(slope), "fp32")
+        assert dz[-1].isnan().all() and db.isnan().all()
+        _, _, db = opr.opr_linear_bwd(dy[:-1], x[:-1], w, zn[:-1], activation, need_dx=False, need_dw=False, bias=True)
+        within(db, np.full(n, slope.sum()), np.full(n, len(slope) * (2.0 ** -19 + 2.0 ** -14)), "fp32")
