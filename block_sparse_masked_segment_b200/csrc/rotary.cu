@@ -67,46 +67,49 @@ template <typename TI, typename TO>
 __global__ void __launch_bounds__(32 * kWarps) heads_kernel(const HeadArgs a, int32_t heads_total) {
   wait_for_previous();
   const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (item >= a.total * heads_total) return;
-  const int64_t tok = item / heads_total;
-  int h = static_cast<int>(item % heads_total), si = 0;
-  while (h >= a.set[si].heads) h -= a.set[si++].heads;
-  const HeadSet& s = a.set[si];
-  const int64_t orow = a.row_map != nullptr ? a.row_map[tok] : tok;
-  if (orow < 0 || orow >= a.total) {
-    if (lane == 0 && a.dev_status != nullptr) atomicOr(a.dev_status, OPR_DEV_BAD_INPUT);
-    return;
-  }
-  const TI* x = static_cast<const TI*>(s.x) + tok * s.x_stride + static_cast<int64_t>(h) * a.d;
-  TO* y = static_cast<TO*>(s.y) + orow * s.y_stride + static_cast<int64_t>(h) * a.d;
-  float rs = 1.f;
-  if (s.mode == kHeadNormRotate) {
-    float sum = 0.f;
-    for (int i = lane; i < a.d; i += 32) sum = fmaf(as_float(x[i]), as_float(x[i]), sum);
-    rs = 1.f / sqrtf(warp_sum(sum) / a.d + a.eps);
-  }
-  auto value = [&](int i) {
-    const float v = as_float(x[i]);
-    return s.mode == kHeadNormRotate ? v * rs * load_typed(s.w, a.w_dtype, i) : v;
-  };
+  const int64_t items = a.total * heads_total;
   bool bad = false;
-  auto put = [&](int i, float v) {
-    y[i] = from_float<TO>(v);
-    bad |= beyond<TO>(as_float(y[i]));
-  };
-  const int pairs = s.mode == kHeadCopy ? 0 : a.pairs;
-  for (int j = lane; j < pairs; j += 32) {
-    float c, sn;
-    turn(a.pos[tok], a.freq[j], a.scale, c, sn);
-    if (a.inverse) sn = -sn;
-    int ia, ib;
-    pair_of(a, j, ia, ib);
-    const float va = value(ia), vb = value(ib);
-    put(ia, va * c - vb * sn);
-    put(ib, vb * c + va * sn);
+  // more than one item a warp only where the grid has all the blocks that a grid can have
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); item < items;
+       item += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t tok = item / heads_total;
+    int h = static_cast<int>(item % heads_total), si = 0;
+    while (h >= a.set[si].heads) h -= a.set[si++].heads;
+    const HeadSet& s = a.set[si];
+    const int64_t orow = a.row_map != nullptr ? a.row_map[tok] : tok;
+    if (orow < 0 || orow >= a.total) {
+      if (lane == 0 && a.dev_status != nullptr) atomicOr(a.dev_status, OPR_DEV_BAD_INPUT);
+      continue;
+    }
+    const TI* x = static_cast<const TI*>(s.x) + tok * s.x_stride + static_cast<int64_t>(h) * a.d;
+    TO* y = static_cast<TO*>(s.y) + orow * s.y_stride + static_cast<int64_t>(h) * a.d;
+    float rs = 1.f;
+    if (s.mode == kHeadNormRotate) {
+      float sum = 0.f;
+      for (int i = lane; i < a.d; i += 32) sum = fmaf(as_float(x[i]), as_float(x[i]), sum);
+      rs = 1.f / sqrtf(warp_sum(sum) / a.d + a.eps);
+    }
+    auto value = [&](int i) {
+      const float v = as_float(x[i]);
+      return s.mode == kHeadNormRotate ? v * rs * load_typed(s.w, a.w_dtype, i) : v;
+    };
+    auto put = [&](int i, float v) {
+      y[i] = from_float<TO>(v);
+      bad |= beyond<TO>(as_float(y[i]));
+    };
+    const int pairs = s.mode == kHeadCopy ? 0 : a.pairs;
+    for (int j = lane; j < pairs; j += 32) {
+      float c, sn;
+      turn(a.pos[tok], a.freq[j], a.scale, c, sn);
+      if (a.inverse) sn = -sn;
+      int ia, ib;
+      pair_of(a, j, ia, ib);
+      const float va = value(ia), vb = value(ib);
+      put(ia, va * c - vb * sn);
+      put(ib, vb * c + va * sn);
+    }
+    for (int i = 2 * pairs + lane; i < a.d; i += 32) put(i, value(i));
   }
-  for (int i = 2 * pairs + lane; i < a.d; i += 32) put(i, value(i));
   if (bad && a.dev_status != nullptr) atomicOr(a.dev_status, OPR_DEV_FP16_RANGE);
 }
 
@@ -724,7 +727,7 @@ cudaError_t launch_heads(const HeadArgs& a, int32_t x_dtype, int32_t y_dtype, cu
   for (int i = 0; i < a.n_sets; ++i) heads += a.set[i].heads;
   if (a.total == 0 || heads == 0) return cudaSuccess;
   if (vector_ready(a, x_dtype, y_dtype, y_dtype)) return launch_heads_vec(a, x_dtype, y_dtype, stream);
-  const int64_t blocks = (a.total * heads + kWarps - 1) / kWarps;
+  const int64_t blocks = std::min<int64_t>((a.total * heads + kWarps - 1) / kWarps, 0x7FFFFFFF);  // of a grid at most
   return with_type(x_dtype, [&](auto ti) {
     return with_type(y_dtype, [&](auto to) {
       return launch_overlapped(heads_kernel<decltype(ti), decltype(to)>, dim3(static_cast<unsigned>(blocks)), 32 * kWarps, 0,

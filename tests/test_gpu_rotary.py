@@ -422,3 +422,28 @@ def test_heads_calls_on_a_side_stream_and_in_a_graph():
         other = step()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(other, held))
+
+
+def test_rotary_of_more_heads_than_a_grid_has_blocks():
+    """2^34 heads and more, eight to a block of the form for odd sizes, would take more blocks than a grid
+    has; the last token's heads are rotated too (in place, 69 GB)."""
+    total, n, d = 2 ** 18 + 1, 65536, 2
+    if torch.cuda.mem_get_info()[0] < 80 * 2 ** 30:
+        torch.cuda.empty_cache()
+        if torch.cuda.mem_get_info()[0] < 80 * 2 ** 30:
+            pytest.skip("needs 80 GB of device memory")
+    x = torch.zeros(total, n, d, dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, total // 2, total - 2, total - 1]
+    rng = np.random.default_rng(30)
+    for r in rows:
+        x[r] = heads(rng, 1, n, d, "bf16")[0]
+    keep = to64(x[rows])
+    pos = torch.arange(5, 5 + total, dtype=torch.int32, device="cuda")
+    freq = torch.ones(1, dtype=torch.float64, device="cuda")
+    st = status()
+    opr.opr_rotary(x, pos, freq, dev_status=st)
+    assert opr.read_status(st) == []
+    within(x[rows], lo.rotate(keep, to64(pos[rows]), to64(freq)), rotary_bound(keep, d, False, 1.0), "bf16")
+    assert not x[2:total // 2:9973].any()
+    del x
+    torch.cuda.empty_cache()
