@@ -62,6 +62,7 @@ std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};  // pipeline-wait limit of 
 
 opr_status record_cuda_error(cudaError_t e) {
   g_cuda_error_text = cudaGetErrorString(e);
+  cudaGetLastError();  // reported here: the caller's next check of its own work must not find it again
   return OPR_CUDA_ERROR;
 }
 

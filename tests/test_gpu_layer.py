@@ -1,6 +1,8 @@
 """The attention layer end to end (OnePassAttentionLayer): projections, norm with rotation, masked
 attention, output projection and residual, forward and backward, against the layer in fp64."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -132,3 +134,26 @@ def test_layer_refuses_other_shapes_and_types():
     for bad in (dict(x=x[:-1]), dict(x=x.half()), dict(w_qkv=wqkv[:255]), dict(w_o=wo[:, :64])):
         with pytest.raises(opr.OprError):
             layer.forward(**{**dict(x=x, w_qkv=wqkv, w_o=wo, q_weight=qw, k_weight=qw), **bad})
+
+
+def test_a_reported_cuda_error_is_not_left_behind():
+    """A launch that fails on the host (into a capture that was ended by a call it forbids) is reported as
+    OPR_CUDA_ERROR; the caller's next check of the runtime's last error, such as torch makes at each of its
+    launches, does not find it again."""
+    lib, runtime = opr.load_library(), ctypes.CDLL("libcudart.so.12")  # the runtime that both use
+    x, y = torch.ones(4, 2, 64, device="cuda"), torch.empty(4, 2, 64, device="cuda")
+    pos, freq = torch.arange(4, dtype=torch.int32, device="cuda"), torch.ones(32, dtype=torch.float64, device="cuda")
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert runtime.cudaStreamCreate(ctypes.byref(stream)) == 0
+    assert runtime.cudaStreamBeginCapture(stream, 0) == 0
+    assert runtime.cudaStreamSynchronize(stream) != 0  # forbidden: the capture is invalid from here
+    runtime.cudaGetLastError()
+    st = lib.opr_rotary(x.data_ptr(), 1, 128, y.data_ptr(), 1, 128, pos.data_ptr(), freq.data_ptr(), 64, 0, 1.0, 0, None,
+                        4, 2, 64, None, stream)
+    left = runtime.cudaGetLastError()
+    runtime.cudaStreamEndCapture(stream, ctypes.byref(graph))
+    runtime.cudaGetLastError()
+    runtime.cudaStreamDestroy(stream)
+    assert st == 3 and b"captur" in lib.opr_last_error() and left == 0
+    assert opr.opr_rotary(x, pos, freq, out=y) is y and (y.isfinite()).all()
