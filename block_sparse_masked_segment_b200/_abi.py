@@ -239,8 +239,9 @@ def layout_table_offsets(lay: "Layout") -> dict[str, int]:
 
 
 def read_status(dev_status: torch.Tensor) -> list[str]:
-    """Synchronise and decode the device status word (empty list = no error)."""
-    v = int(dev_status.item())
+    """Synchronise and decode the device status word, or that of a result which keeps one (``_status``; empty
+    list = no error)."""
+    v = int(getattr(dev_status, "_status", dev_status).item())
     return [name for bit, name in DEV_BITS.items() if v & bit]
 
 
@@ -859,6 +860,13 @@ def _status_word(dev_status, device) -> torch.Tensor:
     return dev_status
 
 
+def _keep_status(status: torch.Tensor, *results: torch.Tensor | None) -> None:
+    """The word stays readable on the results, whoever made it."""
+    for t in results:
+        if t is not None:
+            t._status = status
+
+
 def _scratch(workspace, need: int, device):
     """The caller's workspace, or one of `need` bytes (None for 0): (tensor, bytes)."""
     if workspace is None:
@@ -887,7 +895,8 @@ def opr_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
     ``activation`` None, "silu", "gelu" or "gelu_tanh"; bias [n] and residual [m, n] of bf16, fp16 or fp32.  The
     result has ``out_dtype`` (default: x's type) or is ``out``, which may be the residual.  With ``save_z``
     returns (y, z), z = x w^T + bias in x's type, for opr_linear_bwd.  x, w, residual and out may be parts of
-    wider rows.  ``dev_status`` reports a pipeline timeout or an fp16 overflow (read_status).
+    wider rows.  ``dev_status`` reports a pipeline timeout (the results are then invalid) or an fp16 overflow:
+    read_status(dev_status), or read_status of a result, which keeps the word of its call, given or not.
     """
     ldx, ldw = _matrix("x", x, _MMA_TYPES), _matrix("w", w, (x.dtype,))
     m, k = x.shape
@@ -918,6 +927,7 @@ def opr_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
           0 if bias is None else _DT[bias.dtype], ACTIVATIONS[activation], _ptr(residual), ldr,
           0 if residual is None else _DT[residual.dtype], _ptr(out), ldy, _DT[out.dtype], _ptr(z), n, m, n, k,
           _ptr(workspace), ws_bytes, _ptr(status))
+    _keep_status(status, out, z)
     return (out, z) if save_z else out
 
 
@@ -942,6 +952,7 @@ def opr_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.
     dy, x and w have one type of bf16 or fp16; z is opr_linear's (needed with an activation).  dx and dw have
     ``dx_dtype`` and ``dw_dtype`` (default: x's and w's type) or are the tensors of ``out`` = (dx, dw), parts of
     wider rows allowed; dx may be dx_residual.  The gradient with respect to opr_linear's residual is dy itself.
+    ``dev_status`` as in opr_linear.
     """
     ldx, ldw = _matrix("x", x, _MMA_TYPES), _matrix("w", w, (x.dtype,))
     m, k = x.shape
@@ -982,4 +993,5 @@ def opr_linear_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.
           ACTIVATIONS[activation], _ptr(dx_residual), ldr, 0 if dx_residual is None else _DT[dx_residual.dtype], _ptr(dx),
           ldx_out, 0 if dx is None else _DT[dx.dtype], _ptr(dw), ldw_out, 0 if dw is None else _DT[dw.dtype], _ptr(db),
           m, n, k, _ptr(workspace), ws_bytes, _ptr(status))
+    _keep_status(status, dx, dw, db)
     return dx, dw, db

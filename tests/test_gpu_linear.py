@@ -450,3 +450,30 @@ def test_activations_of_every_bf16_exponent(activation):
         assert dz[-1].isnan().all() and db.isnan().all()
         _, _, db = opr.opr_linear_bwd(dy[:-1], x[:-1], w, zn[:-1], activation, need_dx=False, need_dw=False, bias=True)
         within(db, np.full(n, slope.sum()), np.full(n, len(slope) * (2.0 ** -19 + 2.0 ** -14)), "fp32")
+
+
+def test_results_keep_the_status_word_of_a_call_that_was_given_none():
+    """A timeout and an fp16 overflow are there to read on the results, each call with a word of its own."""
+    rng = np.random.default_rng(31)
+    x, w, dy = matrix(rng, 300, 4096, "bf16"), matrix(rng, 300, 4096, "bf16"), matrix(rng, 300, 300, "bf16")
+    good, z = opr.opr_linear(x, w, save_z=True)
+    assert opr.read_status(good) == [] and opr.read_status(z) == []
+    lib = opr.load_library()
+    torch.cuda.synchronize()
+    prev = lib.opr_testing_set_wait_limit_ns(0)
+    try:
+        y, z = opr.opr_linear(x, w, save_z=True)
+        grads = opr.opr_linear_bwd(dy, x, w, bias=True)
+        torch.cuda.synchronize()
+    finally:
+        lib.opr_testing_set_wait_limit_ns(prev)
+    for t in (y, z, *grads):
+        assert opr.read_status(t) == [_abi.DEV_BITS[8]]
+    assert opr.read_status(good) == []
+    x, w = torch.full((4, 64), 64.0, dtype=torch.float16, device="cuda"), torch.full((8, 64), 16.0, dtype=torch.float16, device="cuda")
+    assert opr.read_status(opr.opr_linear(x, w)) == [_abi.DEV_BITS[16]]
+    out = torch.empty(4, 8, device="cuda")
+    assert opr.read_status(opr.opr_linear(x, w, out=out)) == []
+    # a word that the caller gives is the results' too
+    st = status()
+    assert opr.read_status(opr.opr_linear(x, w, dev_status=st)) == opr.read_status(st) == [_abi.DEV_BITS[16]]
