@@ -87,7 +87,7 @@ __device__ __forceinline__ bool store_typed(void* p, int32_t dtype, int64_t i, f
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
   } else if (dtype == OPR_DTYPE_FP16) {
     static_cast<__half*>(p)[i] = __float2half_rn(v);
-    return !(fabsf(v) <= 65504.f);
+    return beyond_f16(v);
   } else {
     static_cast<float*>(p)[i] = v;
   }
@@ -231,7 +231,7 @@ __device__ __forceinline__ bool store_row(void* p, int32_t dtype, int64_t i, con
       w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
     } else {
       w[k] = pack_f16x2(v[2 * k], v[2 * k + 1]);
-      bad |= !(fabsf(v[2 * k]) <= 65504.f) || !(fabsf(v[2 * k + 1]) <= 65504.f);
+      bad |= beyond_f16(v[2 * k]) || beyond_f16(v[2 * k + 1]);
     }
   }
   *reinterpret_cast<Words*>(static_cast<uint16_t*>(p) + i) = u;
@@ -648,7 +648,7 @@ __device__ __forceinline__ void stage_row16(uint8_t* block, int row, const float
       top = fmaxf(top, fabsf(v[i]));
       nan |= v[i] != v[i];
     }
-    bad |= nan || top > 65504.f;
+    bad |= nan || beyond_f16(top);
   }
 }
 __device__ __forceinline__ void stage_row32(uint8_t* block, int row, const float (&v)[32]) {

@@ -309,7 +309,7 @@ __device__ __forceinline__ void store_unit(T* p, const UnitAt<VW>& at, const uin
 }
 __device__ __forceinline__ bool overflowed(__half2 top) {
   const float2 t = __half22float2(top);
-  return !(t.x <= 65504.f) || !(t.y <= 65504.f);
+  return beyond_f16(t.x) || beyond_f16(t.y);
 }
 
 // Rotates the unit's pairs.  t: for pairs 2i, 2i + 1, t[2i] = (cos, cos), t[2i + 1] = (sin, sin).

@@ -477,3 +477,41 @@ def test_results_keep_the_status_word_of_a_call_that_was_given_none():
     # a word that the caller gives is the results' too
     st = status()
     assert opr.read_status(opr.opr_linear(x, w, dev_status=st)) == opr.read_status(st) == [_abi.DEV_BITS[16]]
+
+
+# sums of 64 products by one: 65504 with 1023.5 each, the largest below fp16's overflow, the first that overflows
+NEAR = {65511.5: {0: 1031.0}, 65519.5: {0: 1039.0}, 65520.0: {0: 1039.0, 1: 1024.0}}
+
+
+@pytest.mark.parametrize("m,n", [(4, 16), (4, 13), (200, 72), (200, 65), (2500, 2304), (2500, 2075)])
+@pytest.mark.parametrize("value", NEAR)
+def test_fp16_overflow_is_that_of_the_stored_value(m, n, value):
+    """Sums up to 65520 round to 65504, which is no overflow; 65520 itself is stored as an infinity."""
+    x, w = torch.ones(m, 64, dtype=torch.float16, device="cuda"), torch.full((n, 64), 1023.5, dtype=torch.float16, device="cuda")
+    for i, v in NEAR[value].items():
+        w[n - 1, i] = v
+    over = value >= 65520
+    for kw in (dict(), dict(save_z=True, out_dtype=torch.float32)):
+        st = status()
+        got = opr.opr_linear(x, w, dev_status=st, **kw)
+        got = got[1] if kw else got
+        assert (got[:, :-1] == 65504).all() and (got[:, -1] == (float("inf") if over else 65504)).all()
+        assert opr.read_status(st) == ([_abi.DEV_BITS[16]] if over else [])
+
+
+@pytest.mark.parametrize("n", [8, 3])
+def test_fp16_overflow_of_a_gradient_behind_an_activation(n):
+    """dz = dy act'(z), silu: entries between 65504 and 65520 by a margin above the slope's error, and past
+    65520."""
+    z = torch.arange(1.0, 4.0, 2.0 ** -9, device="cuda").half()
+    slope = torch.from_numpy(lo.act_slope(to64(z), "silu"))
+    dy = torch.arange(57344.0, 65504.0, 32.0)
+    prod = dy.double()[:, None] * slope
+    x, w = torch.zeros(5, 8, dtype=torch.float16, device="cuda"), torch.zeros(n, 8, dtype=torch.float16, device="cuda")
+    for a, b, over in ((65506, 65518, False), (65522, 65530, True)):
+        i, j = ((prod > a) & (prod < b)).nonzero()[0].tolist()
+        g, zz = torch.zeros(5, n, dtype=torch.float16, device="cuda"), torch.zeros(5, n, dtype=torch.float16, device="cuda")
+        g[4, n - 1], zz[4, n - 1] = dy[i].item(), z[j]
+        st = status()
+        opr.opr_linear_bwd(g, x, w, zz, "silu", dev_status=st)
+        assert opr.read_status(st) == ([_abi.DEV_BITS[16]] if over else [])
