@@ -1035,18 +1035,22 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
 // us for 58 MB, 4.4 TB/s, with the column sums' second kernel).
 constexpr int kDzThreads = 256;
 constexpr int kDzSpan = 32;      // column groups of a block
-constexpr int kDzMaxBlocks = 512;  // row blocks, which sizes the partial sums
+constexpr int kDzRows = kDzThreads / kDzSpan;  // rows at a time
+constexpr int kDzMaxBlocks = 512;  // row blocks that fill the GPU, at most
+constexpr int kDzMaxRun = 256;     // entries that a thread adds in fp32 at most; longer columns take more row blocks,
+                                   // whose sums are added in fp64 (a chain of 4096 lost 2^-13 of its sum)
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const T* dy, int64_t ld_dy, const T* z, int64_t ldz, int64_t m,
+__global__ void __launch_bounds__(kDzThreads, 4) linear_dz_kernel(const T* dy, int64_t ld_dy, const T* z, int64_t ldz, int64_t m,
                                                                int32_t n, int32_t act, T* dz, int64_t ld_dz, float* partial,
                                                                int64_t rows_per_block, int32_t* dev_status) {
   constexpr int32_t kType = std::is_same_v<T, __half> ? OPR_DTYPE_FP16 : OPR_DTYPE_BF16;
-  constexpr int kRows = kDzThreads / kDzSpan;  // rows at a time
+  constexpr int kRows = kDzRows;
   __shared__ float sums[kRows][kDzSpan * W + 1];
   const int col = threadIdx.x % kDzSpan, row = threadIdx.x / kDzSpan;
   const int64_t j = (static_cast<int64_t>(blockIdx.x) * kDzSpan + col) * W;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per_block;
+  const int64_t row_block = blockIdx.y + static_cast<int64_t>(gridDim.y) * blockIdx.z;
+  const int64_t r0 = row_block * rows_per_block;
   const int64_t r1 = r0 + rows_per_block < m ? r0 + rows_per_block : m;
   float sum[W] = {};
   bool bad = false;
@@ -1088,7 +1092,7 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const T* dy, int6
     }
   }
   if (bad && dev_status != nullptr) atomicOr(dev_status, OPR_DEV_FP16_RANGE);
-  if (partial == nullptr) return;
+  if (partial == nullptr || r0 >= m) return;  // r0 >= m: blocks behind the last rows, of a grid with more than one z
 #pragma unroll
   for (int k = 0; k < W; ++k) sums[row][col * W + k] = sum[k];
   __syncthreads();
@@ -1097,7 +1101,7 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const T* dy, int6
     float t = 0.f;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) t += sums[r][c];
-    partial[static_cast<int64_t>(blockIdx.y) * n + first + c] = t;
+    partial[row_block * n + first + c] = t;
   }
 }
 
@@ -1332,7 +1336,8 @@ DzPlan dz_plan(int64_t m, int32_t n, bool wide) {
   p.wide = wide;
   p.cols = static_cast<int32_t>(ceil_div(n, kDzSpan * (wide ? 8 : 1)));
   // row blocks: four blocks an SM in all, eight rows at least to each
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({ceil_div(148 * 4, p.cols), ceil_div(m, 8), kDzMaxBlocks}));
+  const int64_t want = std::max<int64_t>({1, std::min<int64_t>({ceil_div(148 * 4, p.cols), ceil_div(m, 8), kDzMaxBlocks}),
+                                          ceil_div(m, kDzMaxRun * kDzRows)});
   p.rows_per_block = ceil_div(m, want);
   p.rows = m > 0 ? static_cast<int32_t>(ceil_div(m, p.rows_per_block)) : 0;
   return p;
@@ -1350,7 +1355,8 @@ cudaError_t launch_linear_dz(const void* dy, int64_t ld_dy, const void* z, int64
   const bool wide = n % 8 == 0 && fits(dy, ld_dy) && (activation == OPR_ACT_NONE || fits(z, ldz)) && fits(dz, ld_dz);
   const DzPlan plan = dz_plan(m, n, wide);
   if (plan.rows > 0) {
-    const dim3 grid(plan.cols, plan.rows);
+    const int32_t rows_y = std::min(plan.rows, 1 << 15);  // a grid's y has 65535 at most
+    const dim3 grid(plan.cols, rows_y, static_cast<unsigned>(ceil_div(plan.rows, rows_y)));
     float* part = db != nullptr ? partial : nullptr;
     auto go = [&](auto type, auto width) {
       using T = decltype(type);

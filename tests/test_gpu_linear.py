@@ -515,3 +515,29 @@ def test_fp16_overflow_of_a_gradient_behind_an_activation(n):
         st = status()
         opr.opr_linear_bwd(g, x, w, zz, "silu", dev_status=st)
         assert opr.read_status(st) == ([_abi.DEV_BITS[16]] if over else [])
+
+
+@pytest.mark.parametrize("n,m", [(18945, 32768), (151552, 8192)], ids=["entry by entry", "sixteen bytes"])
+def test_column_sums_of_many_rows_under_wide_outputs(n, m):
+    """So many columns that all rows could be one block's, eight threads to them: 2^8 in each thread's first
+    row, then 2^-17, which a running fp32 sum would drop every time.  At most 256 entries are added to one fp32
+    sum (each addition off by at most 2^-24 of the sum so far), the parts in fp64, and the eight threads'
+    results in fp32: (256 + 8) 2^-24 of the sum of sizes."""
+    dy = torch.full((m, n), 2.0 ** -17, dtype=torch.bfloat16, device="cuda")
+    dy[:8] = 2.0 ** 8
+    x, w = torch.zeros(m, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+    _, _, db = opr.opr_linear_bwd(dy, x, w, bias=True, need_dx=False, need_dw=False)
+    want = 8 * 2.0 ** 8 + (m - 8) * 2.0 ** -17
+    within(db, np.full(n, want), np.full(n, 264 * 2.0 ** -24 * want), "fp32")
+
+
+@pytest.mark.parametrize("n", [3, 8])
+def test_column_sums_of_more_row_blocks_than_a_grid_is_high(n):
+    """2048 rows at most to a block, 2^15 blocks to each z of the grid: ones, which sum exactly up to the
+    result's rounding; the last rows, which lie in the second z, count 3."""
+    m = 2 ** 26 + 4099
+    dy = torch.ones(m, n, dtype=torch.bfloat16, device="cuda")
+    dy[-4000:] = 3
+    x, w = torch.zeros(m, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+    _, _, db = opr.opr_linear_bwd(dy, x, w, bias=True, need_dx=False, need_dw=False)
+    within(db, np.full(n, m + 2.0 * 4000), np.zeros(n), "fp32")
