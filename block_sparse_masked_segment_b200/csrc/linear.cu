@@ -63,9 +63,10 @@ __device__ __forceinline__ float activate(float z, int32_t act) {
 
 // The slopes have reached 0 or 1 at |z| = 128 in fp32, and further out their terms
 // overflow (z^3 from 2^43 on, the infinities at once) and would meet those zeros as NaN:
-// z is held to +-128, NaN stays.
+// z is held to +-128; NaN stays.
 __device__ __forceinline__ float activate_slope(float z, int32_t act) {
-  z = z < -128.f ? -128.f : z > 128.f ? 128.f : z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(z), "f"(-128.f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(z), "f"(128.f));
   if (act == OPR_ACT_SILU) {
     const float s = sigmoid(z);
     return s * (1.f + z * (1.f - s));
