@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(32 * kWarps) head_grads_kernel(const HeadArgs 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const HeadSet& s = a.set[blockIdx.y];
   for (int i = lane; i < a.d; i += 32) sums[warp][i] = 0.f;
+  __syncwarp();  // an entry's sums are not added by the lane that cleared it
   bool bad = false;
   const int64_t items = a.total * s.heads;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items;

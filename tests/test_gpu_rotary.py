@@ -447,3 +447,24 @@ def test_rotary_of_more_heads_than_a_grid_has_blocks():
     assert not x[2:total // 2:9973].any()
     del x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("d,rot", [(80, 20), (72, 64), (18, 6), (200, 104)])
+def test_weight_gradients_of_odd_sizes_repeat(d, rot):
+    """In the form for odd sizes the lane that adds to an entry's sum is another than the one that clears it
+    (interleaved pairs): blocks of one head or a few, whose sums follow the clearing at once, many times;
+    against the formula, and the same bits each time."""
+    rng = np.random.default_rng(50)
+    for total in (1, 40):
+        q, k, _ = qkv(rng, total, 3, 1, d, "bf16", False)
+        dq, dk = heads(rng, total, 3, d, "fp32"), heads(rng, total, 1, d, "fp32")
+        qw, kw = weights(rng, d, "bf16")
+        pos = positions(rng, total)
+        freq, _ = opr.opr_rotary_frequencies(rot, 1e4)
+        first = opr.opr_qk_norm_rope_bwd(dq, dk, q, k, qw, kw, pos, freq, EPS, True)
+        for got, dy, x, w in ((first[2], dq, q, qw), (first[3], dk, k, kw)):
+            _, rw = lo.norm_rotate_bwd(to64(dy), to64(x), to64(w), to64(pos), to64(freq), EPS, True)
+            within(got, rw, grad_bounds(to64(dy), to64(x), to64(w), to64(pos), to64(freq), True, 1.0)[1], "fp32")
+        for _ in range(100):
+            again = opr.opr_qk_norm_rope_bwd(dq, dk, q, k, qw, kw, pos, freq, EPS, True)
+            assert all(torch.equal(a, b) for a, b in zip(again, first))
