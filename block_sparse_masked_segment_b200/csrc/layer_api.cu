@@ -26,14 +26,20 @@ struct Rows {
   bool same(const Rows& o) const { return p == o.p && dtype == o.dtype && stride == o.stride; }
 };
 
+// An array of n 32-bit words as one row.
+Rows words(const void* p, int64_t n) { return {p, 1, n, n, OPR_DTYPE_FP32}; }
+
 // May the two share memory?  Blocks of rows with one stride, side by side in
-// wider rows, do not although their ranges do.
+// wider rows, do not although their ranges do, nor does a single row between those
+// of a block.
 bool overlap(const Rows& a, const Rows& b) {
   if (a.p == nullptr || b.p == nullptr || a.bytes() == 0 || b.bytes() == 0) return false;
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
   if (pa + static_cast<uint64_t>(a.bytes()) <= pb || pb + static_cast<uint64_t>(b.bytes()) <= pa) return false;
-  if (a.step() != b.step()) return true;
-  const int64_t step = a.step(), wa = a.width * dtype_bytes(a.dtype), wb = b.width * dtype_bytes(b.dtype);
+  if (a.rows == 1 && b.rows == 1) return true;
+  if (a.rows != 1 && b.rows != 1 && a.step() != b.step()) return true;
+  const int64_t step = a.rows == 1 ? b.step() : a.step();
+  const int64_t wa = a.width * dtype_bytes(a.dtype), wb = b.width * dtype_bytes(b.dtype);
   const int64_t diff = pb >= pa ? static_cast<int64_t>((pb - pa) % static_cast<uint64_t>(step))
                                 : step - 1 - static_cast<int64_t>((pa - pb - 1) % static_cast<uint64_t>(step));
   return !(diff >= wa && diff + wb <= step);
@@ -165,7 +171,10 @@ opr_status opr_rotary(const void* x, int32_t x_dtype, int64_t x_stride, void* y,
   if (total_tokens == 0 || n_heads == 0) return OPR_OK;
   if (!x || !y || !pos_id || !freq || !element_aligned(x, x_dtype) || !element_aligned(y, y_dtype))
     return OPR_INVALID_ARG;
-  const Rows in[1] = {{x, total_tokens, x_stride, width, x_dtype}};
+  const Rows in[4] = {{x, total_tokens, x_stride, width, x_dtype},
+                      words(pos_id, total_tokens),
+                      words(freq, rot_dim),  // rot_dim / 2 of 64 bits
+                      words(row_map, total_tokens)};
   const OutRows out[1] = {{{y, total_tokens, y_stride, width, y_dtype}, {row_map ? nullptr : &in[0], nullptr}}};
   if (outputs_clash(in, out)) return OPR_INVALID_ARG;
   const opr_status st = device_check();
@@ -204,11 +213,14 @@ opr_status opr_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
   for (const void* p : {q_out, k_out, v_out})
     if (!element_aligned(p, y_dtype)) return OPR_INVALID_ARG;
   if (!element_aligned(q_weight, w_dtype) || !element_aligned(k_weight, w_dtype)) return OPR_INVALID_ARG;
-  const Rows in[5] = {{q, total_tokens, q_stride, wq, x_dtype},
+  const Rows in[8] = {{q, total_tokens, q_stride, wq, x_dtype},
                       {k, total_tokens, k_stride, wkv, x_dtype},
                       {v, total_tokens, v_stride, wkv, x_dtype},
                       {q_weight, 1, head_dim, head_dim, w_dtype},
-                      {k_weight, 1, head_dim, head_dim, w_dtype}};
+                      {k_weight, 1, head_dim, head_dim, w_dtype},
+                      words(pos_id, total_tokens),
+                      words(freq, rot_dim),
+                      words(row_map, total_tokens)};
   const bool in_place = row_map == nullptr;
   const OutRows out[3] = {{{q_out, total_tokens, wq, wq, y_dtype}, {in_place ? &in[0] : nullptr, nullptr}},
                           {{k_out, total_tokens, wkv, wkv, y_dtype}, {in_place ? &in[1] : nullptr, nullptr}},
@@ -276,10 +288,12 @@ opr_status opr_qk_norm_rope_bwd(const void* dq, const void* dk, const void* dv, 
   for (const void* p : {dq_out, dk_out, dv_out})
     if (!element_aligned(p, dx_dtype)) return OPR_INVALID_ARG;
   const int64_t n = total_tokens;
-  const Rows in[7] = {{dq, n, wq, wq, dy_dtype},     {dk, n, wkv, wkv, dy_dtype},
+  const Rows in[10] = {{dq, n, wq, wq, dy_dtype},    {dk, n, wkv, wkv, dy_dtype},
                       {dv, n, wkv, wkv, dy_dtype},   {q, n, q_stride, wq, x_dtype},
                       {k, n, k_stride, wkv, x_dtype}, {q_weight, 1, head_dim, head_dim, w_dtype},
-                      {k_weight, 1, head_dim, head_dim, w_dtype}};
+                      {k_weight, 1, head_dim, head_dim, w_dtype},
+                      words(pos_id, n),              words(freq, rot_dim),
+                      words(row_map, n)};
   const Rows* own_dy[3] = {&in[0], &in[1], &in[2]};
   if (row_map != nullptr) own_dy[0] = own_dy[1] = own_dy[2] = nullptr;
   const int64_t ws_words = static_cast<int64_t>(workspace_bytes / sizeof(float));

@@ -468,3 +468,18 @@ def test_weight_gradients_of_odd_sizes_repeat(d, rot):
         for _ in range(100):
             again = opr.opr_qk_norm_rope_bwd(dq, dk, q, k, qw, kw, pos, freq, EPS, True)
             assert all(torch.equal(a, b) for a, b in zip(again, first))
+
+
+def test_positions_between_the_rows_of_an_output():
+    """What lies between the rows of a wider buffer is no part of the output: positions and table there are
+    taken, and keep their values."""
+    rng = np.random.default_rng(51)
+    total, n, d = 6, 2, 64
+    buf = torch.zeros(total, 512, device="cuda")
+    x, out = heads(rng, total, n, d, "fp32"), buf[:, :n * d].unflatten(1, (n, d))
+    pos, freq = buf[0, 200:200 + total].view(torch.int32), buf[1, 256:256 + d].view(torch.float64)
+    p, f = positions(rng, total), opr.opr_rotary_frequencies(d, 1e4)[0]
+    pos.copy_(p), freq.copy_(f)
+    opr.opr_rotary(x, pos, freq, out=out)
+    within(out, lo.rotate(to64(x), to64(p), to64(f)), rotary_bound(to64(x), d, False, 1.0), "fp32")
+    assert torch.equal(pos, p) and torch.equal(freq, f)

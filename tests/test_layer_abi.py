@@ -173,6 +173,27 @@ def test_linear_gradient_refusals(lib, kw, want):
     assert lin_bwd(lib, **kw) == want
 
 
+@pytest.mark.parametrize("kw", [
+    dict(y=at(1)), dict(y=at(2)), dict(y=at(3), row_map=at(3)), dict(y=at(1), pos=ctypes.c_void_p((1 << 20) + 5080)),
+    dict(y=ctypes.c_void_p((2 << 20) + 248), yt=FP32, ys=256),             # the table's last entry
+    dict(y=at(1), ys=512, pos=ctypes.c_void_p((1 << 20) + 1000)),          # positions that reach into the second row
+])
+def test_rotary_refuses_outputs_over_positions_table_and_map(lib, kw):
+    assert rotary(lib, **kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(qo=at(3)), dict(ko=at(4)), dict(vo=at(5), row_map=at(5)), dict(qo=at(4)),
+                                dict(ko=at(5), row_map=at(5))])
+def test_qk_norm_refuses_outputs_over_positions_table_and_map(lib, kw):
+    assert qk(lib, **kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(dqo=at(3)), dict(dko=at(4)), dict(dvo=at(7), row_map=at(7)), dict(dqw=at(4)),
+                                dict(dkw=at(3)), dict(ws=at(4)), dict(ws=at(7), row_map=at(7))])
+def test_qk_norm_gradient_refuses_outputs_over_positions_table_and_map(lib, kw):
+    assert qk_bwd(lib, **kw) == INVALID
+
+
 def test_binding_refuses_tensors_off_the_gpu():
     x = torch.zeros(4, 2, 64)
     pos, freq = torch.zeros(4, dtype=torch.int32), torch.ones(32, dtype=torch.float64)
