@@ -49,7 +49,14 @@ bool element_aligned(const void* p, int32_t dtype) {
   return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(dtype_bytes(dtype)) == 0;
 }
 
+// Arrays of 32 and of 64 bits, null allowed.
+bool words_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool doubles_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
 // What the three calls on heads check alike.
+bool head_arrays_ok(const int32_t* pos_id, const double* freq, const int32_t* row_map, const int32_t* dev_status) {
+  return words_aligned(pos_id) && doubles_aligned(freq) && words_aligned(row_map) && words_aligned(dev_status);
+}
 bool head_args_ok(int64_t total, int32_t head_dim, int32_t rot_dim, float scale) {
   return total >= 0 && total < kMaxRows && head_dim >= 2 && head_dim <= 256 && rot_dim >= 2 && rot_dim % 2 == 0 &&
          rot_dim <= head_dim && std::isfinite(scale);
@@ -169,7 +176,8 @@ opr_status opr_rotary(const void* x, int32_t x_dtype, int64_t x_stride, void* y,
   const int64_t width = static_cast<int64_t>(n_heads) * head_dim;
   if (x_stride < width || y_stride < width) return OPR_INVALID_ARG;
   if (total_tokens == 0 || n_heads == 0) return OPR_OK;
-  if (!x || !y || !pos_id || !freq || !element_aligned(x, x_dtype) || !element_aligned(y, y_dtype))
+  if (!x || !y || !pos_id || !freq || !element_aligned(x, x_dtype) || !element_aligned(y, y_dtype) ||
+      !head_arrays_ok(pos_id, freq, row_map, dev_status))
     return OPR_INVALID_ARG;
   const Rows in[4] = {{x, total_tokens, x_stride, width, x_dtype},
                       words(pos_id, total_tokens),
@@ -212,7 +220,9 @@ opr_status opr_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
     if (!element_aligned(p, x_dtype)) return OPR_INVALID_ARG;
   for (const void* p : {q_out, k_out, v_out})
     if (!element_aligned(p, y_dtype)) return OPR_INVALID_ARG;
-  if (!element_aligned(q_weight, w_dtype) || !element_aligned(k_weight, w_dtype)) return OPR_INVALID_ARG;
+  if (!element_aligned(q_weight, w_dtype) || !element_aligned(k_weight, w_dtype) ||
+      !head_arrays_ok(pos_id, freq, row_map, dev_status))
+    return OPR_INVALID_ARG;
   const Rows in[8] = {{q, total_tokens, q_stride, wq, x_dtype},
                       {k, total_tokens, k_stride, wkv, x_dtype},
                       {v, total_tokens, v_stride, wkv, x_dtype},
@@ -279,7 +289,7 @@ opr_status opr_qk_norm_rope_bwd(const void* dq, const void* dk, const void* dv, 
   if (total_tokens > 0 && (!dq || !dk || !q || !k || !pos_id || !freq || !dq_out || !dk_out)) return OPR_INVALID_ARG;
   if (!aligned16(workspace) || !element_aligned(dq_weight, OPR_DTYPE_FP32) ||
       !element_aligned(dk_weight, OPR_DTYPE_FP32) || !element_aligned(q_weight, w_dtype) ||
-      !element_aligned(k_weight, w_dtype))
+      !element_aligned(k_weight, w_dtype) || !head_arrays_ok(pos_id, freq, row_map, dev_status))
     return OPR_INVALID_ARG;
   for (const void* p : {dq, dk, dv})
     if (!element_aligned(p, dy_dtype)) return OPR_INVALID_ARG;
@@ -354,7 +364,7 @@ opr_status opr_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
   if (!known_dtype(y_dtype) || (bias && !known_dtype(bias_dtype)) || (residual && !known_dtype(residual_dtype)))
     return OPR_UNSUPPORTED;
   if (m == 0) return OPR_OK;
-  if (!x || !w || !y || !dev_status) return OPR_INVALID_ARG;
+  if (!x || !w || !y || !dev_status || !words_aligned(dev_status)) return OPR_INVALID_ARG;
   if (!element_aligned(x, dtype) || !element_aligned(w, dtype) || !element_aligned(y, y_dtype) ||
       !element_aligned(z, dtype) || (bias && !element_aligned(bias, bias_dtype)) ||
       (residual && !element_aligned(residual, residual_dtype)))
@@ -430,7 +440,7 @@ opr_status opr_linear_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t 
   if (act && ldz < n) return OPR_INVALID_ARG;
   if (!dx && !dw && !db) return OPR_OK;
   if (m > 0 && (!dy || !x || !w || (act && !z))) return OPR_INVALID_ARG;
-  if (!dev_status || (dx_residual && !dx)) return OPR_INVALID_ARG;
+  if (!dev_status || !words_aligned(dev_status) || (dx_residual && !dx)) return OPR_INVALID_ARG;
   if (!element_aligned(dy, dtype) || !element_aligned(x, dtype) || !element_aligned(w, dtype) ||
       (act && !element_aligned(z, dtype)) || (dx && !element_aligned(dx, dx_dtype)) ||
       (dw && !element_aligned(dw, dw_dtype)) || !element_aligned(db, OPR_DTYPE_FP32) ||

@@ -194,6 +194,23 @@ def test_qk_norm_gradient_refuses_outputs_over_positions_table_and_map(lib, kw):
     assert qk_bwd(lib, **kw) == INVALID
 
 
+def off(mib, by):
+    return ctypes.c_void_p((mib << 20) + by)
+
+
+@pytest.mark.parametrize("kw", [dict(pos=off(1, 2)), dict(freq=off(2, 4)), dict(row_map=off(3, 1)), dict(st=off(4, 2))])
+def test_head_calls_refuse_arrays_off_their_elements(lib, kw):
+    """An address inside an element would end the process on the device."""
+    assert rotary(lib, **kw) == INVALID
+    kw = {k: off(v.value >> 20 << 3, v.value & 15) for k, v in kw.items()}  # elsewhere: apart from the weights
+    assert qk(lib, **kw) == INVALID and qk_bwd(lib, **kw) == INVALID
+
+
+@pytest.mark.parametrize("by", [1, 2])
+def test_products_refuse_a_status_word_off_its_element(lib, by):
+    assert lin(lib, st=off(2, by)) == INVALID and lin_bwd(lib, st=off(2, by)) == INVALID
+
+
 def test_binding_refuses_tensors_off_the_gpu():
     x = torch.zeros(4, 2, 64)
     pos, freq = torch.zeros(4, dtype=torch.int32), torch.ones(32, dtype=torch.float64)
