@@ -483,3 +483,21 @@ def test_positions_between_the_rows_of_an_output():
     opr.opr_rotary(x, pos, freq, out=out)
     within(out, lo.rotate(to64(x), to64(p), to64(f)), rotary_bound(to64(x), d, False, 1.0), "fp32")
     assert torch.equal(pos, p) and torch.equal(freq, f)
+
+
+@pytest.mark.parametrize("d,rot", [(128, 128), (64, 32), (80, 20), (18, 6)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_qk_norm_gradient_over_its_inputs(d, rot, packed):
+    """dq and dk written over q and k themselves (one type, one stride), v's gradient beside them where the
+    three are parts of one projection: as into buffers of their own."""
+    rng = np.random.default_rng(52)
+    total, hq, hkv = 300, 4, 2
+    q, k, v = qkv(rng, total, hq, hkv, d, "bf16", packed)
+    dq, dk, dv = (heads(rng, total, h, d, "fp32", scale=0.1) for h in (hq, hkv, hkv))
+    qw, kw = weights(rng, d, "bf16")
+    pos = positions(rng, total)
+    freq, _ = opr.opr_rotary_frequencies(rot, 1e4)
+    args = (qw, kw, pos, freq, EPS, True)
+    want = opr.opr_qk_norm_rope_bwd(dq, dk, q, k, *args, dv=dv)
+    got = opr.opr_qk_norm_rope_bwd(dq, dk, q, k, *args, dv=dv, out=(q, k, v))
+    assert got[0] is q and all(torch.equal(a, b) for a, b in zip(got, want))
