@@ -22,7 +22,7 @@ _LIB_PATH = os.path.join(_HERE, "lib", "libopr_debug.so" if os.environ.get("OPR_
 
 OPR_OK, OPR_INVALID_ARG, OPR_UNSUPPORTED, OPR_CUDA_ERROR, OPR_WORKSPACE_TOO_SMALL = 0, 1, 2, 3, 4
 DEV_BITS = {1: "bad input", 2: "total mismatch", 4: "sequence longer than max_seqlen", 8: "pipeline wait timeout",
-            16: "fp16 range exceeded (rope output or backward fp16 copy)",
+            16: "fp16 range exceeded (an fp16 output or the backward's fp16 copies)",
             32: "layout-table index out of range (debug checks)"}
 DTYPE_BF16, DTYPE_FP32, DTYPE_FP16 = 0, 1, 2
 TILE = 128

@@ -8,10 +8,11 @@
 // 128 x 64 (the weight on the 128 rows where x has few) with the depth of each split
 // over a cluster.  Measured (device us; a library's product of the same sizes in
 // brackets; 1645.8 TFLOP/s is the measured peak):
-//   16384 x 6144 x 4096           535  1.54 PFLOP/s  [546]    at the power limit
+//   16384 x 6144 x 4096           535  1.54 PFLOP/s  [546]    in short runs; 620 call after call, at the
+//                                                             power limit
 //   dx, dw of 16384 x 4096 x 4096 350, 381           [350, 352]  dw: 3.5 waves of tiles
-//   777 x 4096 x 4096              28  0.92 PFLOP/s           fetches from L2
-//   one row, 6144 x 4096         12.3  4.1 TB/s      [11.9]   latency of start and join
+//   777 x 4096 x 4096              28  0.92 PFLOP/s           64 tiles on 74 pairs, start and end of the tile
+//   one row, 6144 x 4096         11.8  4.3 TB/s      [11.9]   latency of start and join
 //   777 x 1000 x 1112            10.2                [6.2]    latency of start and join
 // Tried and slower: the last wave's tiles shared out along the depth over all pairs, the
 // parts joined through L2 (dw 433: pairs at different depths share no rows in L2, and
@@ -37,7 +38,8 @@ constexpr float kGeluC = 0.79788456080286536f, kGeluA = 0.044715f, kSqrtHalf = 0
 
 // Phi(z), the normal distribution function, and e = exp(-z^2 / 2): with x = |z| / sqrt 2,
 // 1 - erf(x) = (a1 t + ... + a5 t^5) e, t = 1 / (1 + p x) (Abramowitz and Stegun 7.1.26,
-// within 1.5e-7).  With erff the products with this activation took up to 1.2 times as
+// within 1.5e-7 of 1: GELU of -3 is off by 5e-5 of its value, of -4 by 5e-4, where 1 + erff
+// makes 1e-6 and 3e-4; further out it is the better of the two).  With erff the products with this activation took up to 1.2 times as
 // long (dz of 2377 x 4096: 22 against 18 us).
 __device__ __forceinline__ float normal(float z, float& e) {
   const float x = fabsf(z) * kSqrtHalf;
@@ -569,9 +571,11 @@ __global__ void __launch_bounds__(kProductThreads, 2)
 // ---------------------------------------------------------------- large products
 // Persistent CTA pairs: one 256 x 256 tile at a time per pair (cta_group::2), each
 // CTA staging its own 128 rows of P and 128 of Q, so that a pair reads each staged
-// byte once where two CTAs of their own would read Q twice (what the SMs can fetch
-// from L2, about 50 bytes a clock each, is the bound: tiles of 256 x 128 and 256 x 64
-// were never the fastest).  Two accumulators: the epilogue of a tile runs while the
+// byte once where two CTAs of their own would read Q twice (at the tensor cores' full rate
+// an SM then takes in 64 bytes a clock; with tiles of 256 x 128 96, and those and 256 x 64
+// were never the fastest).  Few tiles leave pairs idle: 2377 x 1024 over 4096 are 40 tiles,
+// and its 28 us have the tensor pipes of those 80 SMs active 59 % of the time, the fetches
+// from L2 at a third of their ports.  Two accumulators: the epilogue of a tile runs while the
 // next one is multiplied.
 constexpr int kPairTile = 256;
 constexpr int kEpiWarps = 8;
@@ -1032,8 +1036,9 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
 // rows, taken before dz is rounded.  A thread takes W neighbouring columns (eight
 // where the rows allow 16-byte accesses, else one); the block's 256 threads are `wide`
 // column groups times 256 / wide rows, whose sums are added in order at the end.
-// HBM-bound: dy and z are read once, dz written once (2377 x 4096 with SiLU and db: 13.3
-// us for 58 MB, 4.4 TB/s, with the column sums' second kernel).
+// dy and z are read once, dz written once (2377 x 4096 with SiLU and db: 13.1 us by itself,
+// caches cold, for 58 MB, 4.5 TB/s, and 5 for the column sums' second kernel; holding z
+// within the slopes' range is 5 % of it).
 constexpr int kDzThreads = 256;
 constexpr int kDzSpan = 32;      // column groups of a block
 constexpr int kDzRows = kDzThreads / kDzSpan;  // rows at a time

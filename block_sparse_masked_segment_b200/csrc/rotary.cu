@@ -14,8 +14,8 @@
 // instructions (16 entries a lane: the packed arithmetic, the tables and the fast
 // quotients are there for that).  Measured (device time; a plain copy of as many bytes
 // in brackets):
-//   16384 tokens x 32 heads of 128, half of each rotated, bf16 to fp16   50 us, 5.4 TB/s
-//   32749 tokens x 8 heads of 128, fp32, interleaved                     46 us, 5.8 TB/s
+//   16384 tokens x 32 heads of 128, half of each rotated, bf16 to fp16   49 us, 5.5 TB/s
+//   32749 tokens x 8 heads of 128, fp32, interleaved                     45 us, 5.9 TB/s
 //   16384 tokens, 32q/8kv heads of 128 and v, norm                       80 us, 5.0 TB/s [71 us]
 //   65536 tokens, 64q/8kv heads of 128 and v, fp32 gradients            838 us, 6.2 TB/s [824 us]
 // Tried and slower: persistent blocks that make the next tile's tables between rounds
@@ -61,8 +61,10 @@ __device__ __forceinline__ void pair_of(const HeadArgs& a, int j, int& ia, int& 
 }
 
 // One warp per (token, head), entry by entry: any head_dim, stride and alignment.  What
-// the vector form below does not take (odd sizes and strides), at a third to a fifth of
-// its speed.
+// the vector form below does not take: widths that are no multiple of 16, rotated pairs
+// that are no multiple of 8 (20 or 40 entries of a head of 80, 24 of 96), rows off the
+// 16-byte grid.  At a quarter to a fifth of its speed (16384 tokens x 32 heads of 80, 20
+// entries rotated: 193 us, with 16 37), each angle formed anew for every head.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(32 * kWarps) heads_kernel(const HeadArgs a, int32_t heads_total) {
   wait_for_previous();
@@ -408,7 +410,11 @@ struct Quotients {
 // A block takes `tokens` tokens, forms their cos and sin once, and its groups of G
 // lanes walk each set's (token, head) items in rounds, the next round's loads in
 // flight.
-// NORM: the sets of opr_qk_norm_rope; else the one set of opr_rotary.
+// NORM: the sets of opr_qk_norm_rope; else the one set of opr_rotary.  At four blocks an SM
+// the forms with the norm keep 52 to 70 bytes a thread outside the registers, with fp32
+// inputs 262 to 278; they run at the same share of a plain copy's rate either way (16384
+// tokens, 32q/8kv and v: bf16 to fp16 76 us, a copy of as many bytes 63; fp32 to fp32 138
+// and 123).
 template <typename TI, typename TO, int VW, int G, bool NORM>
 __global__ void __launch_bounds__(kThreadsVec, 4) heads_vec_kernel(const HeadArgs a, const Quotients quot, int32_t tokens) {
   constexpr int kGroups = kThreadsVec / G;
@@ -524,7 +530,8 @@ __global__ void __launch_bounds__(kThreadsVec, 2) head_grads_vec_kernel(const He
   uint64_t acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0;
-  // the weight, for the lanes to read back by unit: registers for it would spill
+  // the weight, for the lanes to read back by unit: next to the sums there are no registers
+  // left for it
   float4* wt = reinterpret_cast<float4*>(red + kGroups * a.d);  // [4][units]
   if (!copy && threadIdx.x < G && live) {
     uint64_t w[8];

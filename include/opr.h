@@ -58,7 +58,8 @@ typedef int32_t opr_status;
 #define OPR_DEV_SEQ_TOO_LONG 4     /* a sequence is longer than max_seqlen */
 #define OPR_DEV_WAIT_TIMEOUT 8     /* a pipeline wait exceeded its time limit; outputs are invalid */
 #define OPR_DEV_FP16_RANGE 16      /* an fp16 value beyond +-65504 was written (opr_rope output, or the
-                                      backward's fp16 copies of the scaled dO and of v) */
+                                      backward's fp16 copies of the scaled dO and of v); the operators
+                                      around the attention: an infinity or NaN was stored as fp16 */
 #define OPR_DEV_BOUNDS 32          /* debug library (libopr_debug.so, built with OPR_DEBUG_CHECKS) only:
                                       an index an attention kernel takes from the layout tables (tile id,
                                       sequence bounds, tile-list length or entry) is out of range; the
@@ -558,7 +559,8 @@ OPR_API opr_status opr_rotary_frequencies(int32_t rot_dim, double base, int32_t 
  *             (an entry named twice leaves either row, or parts of both, there).  An entry out of
  *             range sets OPR_DEV_BAD_INPUT and its row is not written.
  *   dev_status  may be NULL; otherwise also OPR_DEV_FP16_RANGE when an fp16 output overflows
- * y may be x (same type and stride, no row_map); any other overlap is refused.  head_dim 2 .. 256,
+ * y may be x (same type and stride, no row_map); any other overlap is refused, with pos_id, freq and
+ * row_map too (here and in the calls below).  head_dim 2 .. 256,
  * rot_dim even, 2 .. head_dim, at most 65536 heads.  opr_rope is the case of the whole head, the half layout and
  * OPR_ROTARY_PLAIN.
  */
@@ -572,7 +574,8 @@ OPR_API opr_status opr_rotary(const void* x, int32_t x_dtype, int64_t x_stride, 
  * opr_qk_norm_rope - the operands of opr_attn_fwd from the projections, in one pass: each head h
  * of q and k becomes rotate(h / sqrt(mean(h^2) + eps) * weight) with the rotation of opr_rotary,
  * v (may be NULL, then v_out too) is converted, and row t of all goes to row row_map[t]
- * (opr_build_layout's attn_pos; NULL: row t).  fp32 arithmetic, one rounding.
+ * (opr_build_layout's attn_pos; NULL: row t).  fp32 arithmetic, one rounding: the squares of a head
+ * are summed in fp32, and a head whose sum overflows there (entries of 2^60 and more) becomes zeros.
  *   q [total, hq, head_dim], k, v [total, hkv, head_dim]  rows of heads, x_dtype, strides >= heads
  *                         * head_dim
  *   q_weight, k_weight    [head_dim], w_dtype;  eps > 0
@@ -625,7 +628,9 @@ OPR_API opr_status opr_qk_norm_rope_bwd(const void* dq, const void* dk, const vo
  *   z         NULL, or [m, n] of type dtype: x w^T + bias, rounded, for opr_linear_bwd
  * fp32 sums, act and residual on the unrounded sum, one rounding.  The tensor cores drop the bits
  * below the running sum: over k = 4096 products of random signs the sum is off by 4e-6 of its size,
- * over 16384 by 2e-5, which an fp32 y shows and a 16-bit one does not.
+ * over 16384 by 2e-5, over 65536 by 8e-5; products of one sign 8e-5 over 16384 and 4e-4 over 65536.
+ * An fp32 y shows it; of products of one sign a bf16 y hides 2^17 and an fp16 y 2^15.
+ * GELU's Phi is within 1.5e-7 of 1 (5e-5 of the value at z = -3, 5e-4 at -4).
  * Rows that start on 16-byte boundaries are read in place; an x or w with others is copied to the
  * workspace first (opr_linear_workspace_bytes looks at the addresses, not at the data).
  *   workspace 16-byte aligned, may be NULL when 0 bytes are needed; calls that may run at the same
@@ -651,7 +656,8 @@ OPR_API opr_status opr_linear(const void* x, int64_t ldx, const void* w, int64_t
  *   dy [m, n]  dtype;  z as kept by opr_linear (unused and may be NULL without an activation)
  *   dx [m, k], dw [n, k], db [n]  each may be NULL: not computed.  dx_residual [m, k] or NULL;
  *              may be dx (same type and row length).  m = 0 sets dw and db to zero.
- * With an activation dz is rounded to dtype for the two products (the type of their operands).
+ * With an activation dz is rounded to dtype for the two products (the type of their operands), whatever
+ * the types of dx and dw.  act' at an infinite z is its limit, 0 or 1.
  * Workspace, dev_status, alignment and overlap as in opr_linear.
  */
 OPR_API size_t opr_linear_bwd_workspace_bytes(const void* dy, int64_t ld_dy, const void* x, int64_t ldx,
