@@ -39,8 +39,8 @@ constexpr float kGeluC = 0.79788456080286536f, kGeluA = 0.044715f, kSqrtHalf = 0
 // Phi(z), the normal distribution function, and e = exp(-z^2 / 2): with x = |z| / sqrt 2,
 // 1 - erf(x) = (a1 t + ... + a5 t^5) e, t = 1 / (1 + p x) (Abramowitz and Stegun 7.1.26,
 // within 1.5e-7 of 1: GELU of -3 is off by 5e-5 of its value, of -4 by 5e-4, where 1 + erff
-// makes 1e-6 and 3e-4; further out it is the better of the two).  With erff the products with this activation took up to 1.2 times as
-// long (dz of 2377 x 4096: 22 against 18 us).
+// makes 1e-6 and 3e-4; further out it is the better of the two).  With erff the products
+// with this activation took up to 1.2 times as long (dz of 2377 x 4096: 22 against 18 us).
 __device__ __forceinline__ float normal(float z, float& e) {
   const float x = fabsf(z) * kSqrtHalf;
   const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
